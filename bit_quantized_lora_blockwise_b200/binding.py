@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -39,7 +40,8 @@ EXPORTS = ("qlora_status_string", "qlora_abi_version", "qlora_nf4_levels", "qlor
            "qlora_paged_adamw_step", "qlora_paged_adamw_set_reserve", "qlora_paged_adamw_placement",
            "qlora_paged_adamw_location", "qlora_paged_adamw_state_bytes", "qlora_paged_adamw_state",
            "qlora_block_workspace_bytes", "qlora_block_fwd", "qlora_block_bwd", "qlora_quantize_dq",
-           "qlora_debug_fail_allocs")
+           "qlora_debug_fail_allocs", "qlora_dropout", "qlora_grouped_workspace_bytes",
+           "qlora_grouped_linear_fwd", "qlora_grouped_linear_bwd")
 
 BLOCK_STREAMS = 2
 
@@ -55,6 +57,30 @@ class LinearDesc(ctypes.Structure):
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1}
 
 NOALLOC_SCRATCH_BYTES = 8 << 20
+MAX_EXPERTS = 1024
+
+# qlora_element of qlora_dropout's tensors
+_ELEMENT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class _DropoutDesc(ctypes.Structure):
+    """qlora_dropout_desc."""
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
+
+
+class Dropout(NamedTuple):
+    """Counter-based dropout: probability p in [0, 1), 64-bit seed and counter
+    offset (taken mod 2^64). The same three values give the same mask; a
+    tensor of n elements uses ceil(n / 8) counters from `offset` on."""
+    p: float
+    seed: int
+    offset: int = 0
+
+    def _desc(self):
+        return _DropoutDesc(float(self.p), int(self.seed) & _U64, int(self.offset) & _U64)
+
+
+_U64 = (1 << 64) - 1
 
 
 class QLoRAError(RuntimeError):
@@ -126,6 +152,17 @@ def load(path: str | None = None):
         lib.qlora_block_workspace_bytes.restype = SZ
         for fn in ("qlora_block_fwd", "qlora_block_bwd"):
             getattr(lib, fn).argtypes = [I32, DP, P, P, I32, I64, I32, F32, I32, P, SZ, P]
+            getattr(lib, fn).restype = I32
+        DD = ctypes.POINTER(_DropoutDesc)
+        lib.qlora_dropout.argtypes = [P, P, I64, I32, DD, P]
+        lib.qlora_dropout.restype = I32
+        lib.qlora_grouped_workspace_bytes.argtypes = [I32, I64, I64, I64, I32, I32]
+        lib.qlora_grouped_workspace_bytes.restype = SZ
+        lib.qlora_grouped_linear_fwd.argtypes = [P, P, P, P, P, I32, I32, I64, I64, I64, P, P, P, P, I32, F32, DD,
+                                                 P, P, P, SZ, P]
+        lib.qlora_grouped_linear_bwd.argtypes = [P, P, P, P, P, I32, I32, I64, I64, I64, P, P, P, P, P, P, I32, F32,
+                                                 DD, P, P, P, P, SZ, P]
+        for fn in ("qlora_grouped_linear_fwd", "qlora_grouped_linear_bwd"):
             getattr(lib, fn).restype = I32
         lib.qlora_device_error.argtypes = [I32]
         lib.qlora_device_error.restype = ctypes.c_uint32
@@ -377,11 +414,18 @@ def _workspace(workspace, M, N, K, r, device):
 
 
 def linear_fwd(packed, q, scale2, X, A, B, alpha: float, N: int, K: int, nf4=None, t8=None,
-               Y=None, XA_out=None, workspace=None):
+               Y=None, XA_out=None, workspace=None, dropout: Dropout | None = None):
     """Y = X W'^T + (alpha/r) (X A) B  -> Y [M, N] (and XA_out if given).
 
     The 16-bit tensors are all bf16 or all fp16 (X's dtype decides; fp16
-    goes through qlora_linear_fwd_dt)."""
+    goes through qlora_linear_fwd_dt).
+
+    dropout: adapter dropout, Y = X W'^T + (alpha/r) (D(X) A) B and XA_out =
+    D(X) A (through qlora_grouped_linear_fwd with one expert; a workspace
+    given must then hold grouped_workspace_bytes(1, M, N, K, r, True))."""
+    if dropout is not None:
+        return _grouped_fwd(packed, q, scale2, X, None, A, B, alpha, N, K, dropout, nf4, t8, Y, XA_out, workspace,
+                            _dense_adapters(A, B, N, K))
     M = X.shape[0]
     r = A.shape[1]
     dt = _dtype_of(X, "X")
@@ -430,9 +474,13 @@ def linear_fwd_noalloc(packed, q, scale2, X, A, B, alpha: float, N: int, K: int,
 
 
 def linear_bwd(packed, q, scale2, X, dY, A, B, alpha: float, N: int, K: int, XA=None, nf4=None, t8=None,
-               dX=None, dA=None, dB=None, workspace=None):
+               dX=None, dA=None, dB=None, workspace=None, dropout: Dropout | None = None):
     """-> (dX [M, K], dA [K, r], dB [r, N]); no dW (W is frozen). The 16-bit
-    tensors are all bf16 or all fp16 (X's dtype decides)."""
+    tensors are all bf16 or all fp16 (X's dtype decides). dropout: the
+    forward's (see linear_fwd)."""
+    if dropout is not None:
+        return _grouped_bwd(packed, q, scale2, X, dY, None, A, B, alpha, N, K, XA, dropout, nf4, t8, dX, dA, dB,
+                            workspace, _dense_adapters(A, B, N, K))
     M = X.shape[0]
     r = A.shape[1]
     dt = _dtype_of(X, "X")
@@ -462,6 +510,138 @@ def linear_bwd(packed, q, scale2, X, dY, A, B, alpha: float, N: int, K: int, XA=
                                           _ptr(dX), _ptr(dA), _ptr(dB), _ptr(workspace), workspace.numel(),
                                           _stream()), "qlora_linear_bwd_dt")
     return dX, dA, dB
+
+
+def dropout(x: torch.Tensor, drop: Dropout, out=None) -> torch.Tensor:
+    """D(x): kept elements times 1 / (1 - p), the others 0 (qlora_dropout), for
+    bf16, fp16 and fp32 tensors of any shape; out may be x. The backward of
+    y = D(x) is the same call on dy."""
+    if x.dtype not in _ELEMENT:
+        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
+    _req(x, "x", x.dtype)
+    if out is None:
+        out = torch.empty_like(x)
+    _req(out, "out", x.dtype, tuple(x.shape))
+    _same_device(x, out=out)
+    with torch.cuda.device(x.device):
+        _check(load().qlora_dropout(_ptr(x), _ptr(out), x.numel(), _ELEMENT[x.dtype], drop._desc(), _stream()),
+               "qlora_dropout")
+    return out
+
+
+def grouped_workspace_bytes(E: int, T: int, N: int, K: int, r: int, dropout: bool = False) -> int:
+    """Scratch bytes of grouped_linear_fwd / grouped_linear_bwd (either), and,
+    with E = 1, of linear_fwd / linear_bwd with dropout. 0: shape refused."""
+    return int(load().qlora_grouped_workspace_bytes(E, T, N, K, r, 1 if dropout else 0))
+
+
+def _same_device(ref, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+
+
+def _dense_adapters(A, B, N, K):
+    """Shapes of one expert's adapters given without an expert dimension."""
+    if A.dim() != 2:
+        raise ValueError(f"A must have shape ({K}, r), got {tuple(A.shape)}")
+    r = A.shape[1]
+    return 1, r, (K, r), (r, N)
+
+
+def _expert_adapters(A, B, N, K):
+    if A.dim() != 3:
+        raise ValueError(f"A must have shape (E, {K}, r), got {tuple(A.shape)}")
+    E, _, r = A.shape
+    return E, r, (E, K, r), (E, r, N)
+
+
+def _grouped_checks(packed, q, scale2, X, offsets, A, B, N, K, workspace, drop, shapes):
+    E, r, a_shape, b_shape = shapes
+    T = X.shape[0]
+    dt = _dtype_of(X, "X")
+    _req(packed, "packed", torch.uint8, (E * N * K // 2,))
+    _req(q, "q", torch.uint8, (E * N * K // BLOCK,))
+    _req(scale2, "scale2", torch.float32, (-(-(E * N * K // BLOCK) // DQ_BLOCK),))
+    _req(X, "X", dt, (T, K))
+    _req(A, "A", dt, a_shape)
+    _req(B, "B", dt, b_shape)
+    if offsets is not None:
+        _req(offsets, "offsets", torch.int32, (E + 1,))
+    if workspace is None:
+        need = grouped_workspace_bytes(E, T, N, K, r, drop is not None)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=X.device)
+    _req(workspace, "workspace", torch.uint8)
+    _same_device(X, packed=packed, q=q, scale2=scale2, offsets=offsets, A=A, B=B, workspace=workspace)
+    return E, T, r, dt, workspace
+
+
+def _grouped_fwd(packed, q, scale2, X, offsets, A, B, alpha, N, K, drop, nf4, t8, Y, XA_out, workspace, shapes):
+    E, T, r, dt, workspace = _grouped_checks(packed, q, scale2, X, offsets, A, B, N, K, workspace, drop, shapes)
+    if Y is None:
+        # rows that no expert owns are left as they are: zeros in a buffer made here
+        Y = (torch.zeros if offsets is not None else torch.empty)((T, N), dtype=dt, device=X.device)
+    _req(Y, "Y", dt, (T, N))
+    if XA_out is not None:
+        _req(XA_out, "XA_out", dt, (T, r))
+    _same_device(X, Y=Y, XA_out=XA_out)
+    tb = _tables(nf4, t8)
+    with torch.cuda.device(X.device):
+        _check(load().qlora_grouped_linear_fwd(_ptr(packed), _ptr(q), _ptr(scale2), tb.nf4, tb.t8, _DTYPE[dt], E, T, N,
+                                               K, _ptr(offsets), _ptr(X), _ptr(A), _ptr(B), r, float(alpha),
+                                               None if drop is None else drop._desc(), _ptr(Y), _ptr(XA_out),
+                                               _ptr(workspace), workspace.numel(), _stream()),
+               "qlora_grouped_linear_fwd")
+    return Y
+
+
+def _grouped_bwd(packed, q, scale2, X, dY, offsets, A, B, alpha, N, K, XA, drop, nf4, t8, dX, dA, dB, workspace,
+                 shapes):
+    E, T, r, dt, workspace = _grouped_checks(packed, q, scale2, X, offsets, A, B, N, K, workspace, drop, shapes)
+    _req(dY, "dY", dt, (T, N))
+    if XA is not None:
+        _req(XA, "XA", dt, (T, r))
+    if dX is None:
+        dX = (torch.zeros if offsets is not None else torch.empty)((T, K), dtype=dt, device=X.device)
+    dA = torch.empty_like(A) if dA is None else dA
+    dB = torch.empty_like(B) if dB is None else dB
+    _req(dX, "dX", dt, (T, K))
+    _req(dA, "dA", dt, tuple(A.shape))
+    _req(dB, "dB", dt, tuple(B.shape))
+    _same_device(X, dY=dY, XA=XA, dX=dX, dA=dA, dB=dB)
+    tb = _tables(nf4, t8)
+    with torch.cuda.device(X.device):
+        _check(load().qlora_grouped_linear_bwd(_ptr(packed), _ptr(q), _ptr(scale2), tb.nf4, tb.t8, _DTYPE[dt], E, T, N,
+                                               K, _ptr(offsets), _ptr(X), _ptr(dY), _ptr(A), _ptr(B), _ptr(XA), r,
+                                               float(alpha), None if drop is None else drop._desc(), _ptr(dX), _ptr(dA),
+                                               _ptr(dB), _ptr(workspace), workspace.numel(), _stream()),
+               "qlora_grouped_linear_bwd")
+    return dX, dA, dB
+
+
+def grouped_linear_fwd(packed, q, scale2, X, offsets, A, B, alpha: float, N: int, K: int, nf4=None, t8=None,
+                       Y=None, XA_out=None, workspace=None, dropout: Dropout | None = None) -> torch.Tensor:
+    """The linear of E experts over token rows sorted by expert
+    (qlora_grouped_linear_fwd): Y[rows of e] = X W'_e^T + (alpha/r) (D(X) A_e) B_e.
+
+    packed, q, scale2: the codec of the experts' weights stacked as [E N, K];
+    offsets: int32 [E + 1] on the device, expert e owning the rows
+    offsets[e] .. offsets[e + 1] - 1 (None with one expert: all rows); A [E,
+    K, r], B [E, r, N]. Rows that no expert owns are left as they are in a Y or
+    XA_out that is passed in; a Y made here has zeros there."""
+    return _grouped_fwd(packed, q, scale2, X, offsets, A, B, alpha, N, K, dropout, nf4, t8, Y, XA_out, workspace,
+                        _expert_adapters(A, B, N, K))
+
+
+def grouped_linear_bwd(packed, q, scale2, X, dY, offsets, A, B, alpha: float, N: int, K: int, XA=None, nf4=None,
+                       t8=None, dX=None, dA=None, dB=None, workspace=None, dropout: Dropout | None = None):
+    """Backward of grouped_linear_fwd (qlora_grouped_linear_bwd) -> (dX [T, K],
+    dA [E, K, r], dB [E, r, N]). XA: what the forward saved, or None to
+    recompute it; dropout: the forward's. An expert without rows gets zero
+    adapter gradients; rows that no expert owns are left as they are in a dX
+    that is passed in, and zero in one made here."""
+    return _grouped_bwd(packed, q, scale2, X, dY, offsets, A, B, alpha, N, K, XA, dropout, nf4, t8, dX, dA, dB,
+                        workspace, _expert_adapters(A, B, N, K))
 
 
 def paged_adamw_placement(free_bytes: int, state_bytes: int, reserve_bytes: int, current: int) -> int:

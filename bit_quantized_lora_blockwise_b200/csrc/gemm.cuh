@@ -56,9 +56,29 @@
 // epilogue of one tile overlaps the mainloop of the next. Every wait is bounded (mbar_wait); on a
 // timeout the CTA drains its own copies and MMAs, frees TMEM and returns with
 // the device error word set.
+//
+// Expert groups (GROUPED = true, pairs only). The weight is a stack of
+// experts [E N, K], the tokens are sorted by expert, and a tile belongs to
+// one expert: unit u of the launch is (expert, weight tile, token tile of
+// that expert), found in a table that each CTA builds from the device
+// offsets. A token tile narrower than the configuration's runs MMAs of fewer
+// columns (a multiple of 64), so a ragged tail costs tensor time in
+// proportion; columns past the expert's last token hold its neighbours' rows
+// and are not stored (each column is a sum of its own). How the units are
+// split (whole tiles, by token sub-tile, or over K) is decided here from
+// the unit count, by the rule that the host uses for the dense call.
+//
+// Adapter dropout in dX (SEP = true): dX = dY W' + D(s G A^T), the mask
+// acting on the low-rank sum alone, so that sum has the second accumulator
+// to itself and the epilogue joins the two. A warp's 32 rows are four
+// counters of 8 consecutive k, so lane j evaluates the four counters of token
+// j: 32 keep bits, one per row, broadcast when column j is joined. They are
+// evaluated while the tile's MMAs run.
 #pragma once
 
 #include "codec.cuh"
+#include "dropout.cuh"
+#include "groups.cuh"
 #include "ptx.cuh"
 
 namespace qlora {
@@ -96,15 +116,26 @@ struct GemmArgs {
   int64_t wkb;
   float nf4[16];
   float t8[256];
+  // expert-grouped calls only
+  GroupArgs groups;
+  int expert_rows;    // N: weight rows of one expert
+  DropoutArgs drop;   // SEP: the adapter dropout of dX, over [tokens, rows]
 };
 
-template <int BN_, int ASRC_, int L2_, int BKB_, int SB_, int SA_, int SP_, int NPW_, bool PAIR_, int NTT_ = 1>
+template <int BN_, int ASRC_, int L2_, int BKB_, int SB_, int SA_, int SP_, int NPW_, bool PAIR_, int NTT_ = 1,
+          bool GROUPED_ = false, bool SEP_ = false>
 struct GemmCfg {
   static constexpr int BM = 128, BK = 64, BN = BN_;
   static constexpr int ASRC = ASRC_, L2 = L2_;
   static constexpr int BKB = BKB_, SB = SB_, SA = SA_, SP = SP_, NPW = NPW_;
   static constexpr bool PAIR = PAIR_;
   static constexpr int NTT = NTT_;                 // token sub-tiles (accumulators) per job
+  static constexpr bool GROUPED = GROUPED_;        // tiles of expert groups
+  static constexpr bool SEP = SEP_;                // low-rank sum in accumulator 1, joined under the dropout mask
+  static_assert(!GROUPED_ || (PAIR_ && BN_ == 256 && BKB_ == 1), "grouped tiles run on pairs, one K block per stage");
+  static_assert(!SEP_ || (GROUPED_ && NTT_ == 1), "a separate low-rank sum takes the second accumulator");
+  // accumulator uses per tile, as the phases count them
+  static constexpr int USES = SEP_ ? 2 : NTT_;
   static constexpr int NCTA = PAIR_ ? 2 : 1;       // CTAs per tile
   static constexpr int TILE_ROWS = 128 * NCTA;     // weight rows per tile
   static constexpr int TILE_COLS = BN_ * NTT_;     // tokens per tile
@@ -142,7 +173,8 @@ struct GemmCfg {
   // then the 256-entry 8-bit constant table
   static constexpr int OFF_MISC = ((OFF_BAR + NBARS * 8) + 15) & ~15;
   static constexpr int OFF_T8 = OFF_MISC + 16 + 64;
-  static constexpr int SMEM_BYTES = OFF_T8 + 1024;
+  static constexpr int OFF_GROUPS = OFF_T8 + 1024;
+  static constexpr int SMEM_BYTES = OFF_GROUPS + (GROUPED_ ? kGroupTableBytes : 0);
   static constexpr int WARPS = 7 + NPW_;
   static constexpr int THREADS = WARPS * 32;
   // two accumulators of BN columns: double-buffered tiles (NTT = 1) or the
@@ -161,6 +193,11 @@ struct TileCoord {
   int row0, col0, rc, kb_begin, nmain, nlora;  // rc: (128-row tile, col tile) index
   int split, nsplit, tail;  // K range split of nsplit (1: the whole K); tail: index among the split tiles
   int only;                 // the one token sub-tile this unit computes, or -1 for all
+  // token geometry: sub-tile st, MMA column c <-> token tok_of(st, c)
+  int group;      // expert (0 when dense)
+  int end;        // one past the tile's last token
+  int nst;        // token sub-tiles of this tile
+  int half;       // columns per CTA half of a sub-tile; an MMA has 2 half columns (pairs)
 };
 
 // Tile `tile` of a grid of row_tiles x col_tiles tiles of (128 ncta) rows x
@@ -200,6 +237,33 @@ __device__ __forceinline__ TileCoord tile_coord(const GemmArgs &a, int unit, int
   t.nmain = kb_end - t.kb_begin;
   t.nlora = (t.split == t.nsplit - 1) ? a.lora_kblocks : 0;
   return t;
+}
+
+// How the units of a grouped launch are cut, from the number of tiles and
+// pair slots (as the host plans a dense launch): the tiles of a last,
+// partial round by token sub-tile when that fills idle pairs, or, when there
+// are at most half as many tiles as pairs, every tile over K in ranges of at
+// least 4 blocks.
+struct GroupedPlan {
+  int tiles, units, full_tiles, tail_splits, tail_subtiles;
+};
+__host__ __device__ __forceinline__ GroupedPlan plan_grouped(int tiles, int slots, int kblocks, int ntt) {
+  GroupedPlan p{tiles, tiles, tiles, 1, 1};
+  const int full = tiles / slots * slots, tail = tiles - full;
+  if (full > 0 && tail > 0 && ntt > 1 && tail * ntt <= slots) {
+    p.full_tiles = full;
+    p.tail_subtiles = ntt;
+    p.units = full + tail * ntt;
+  } else if (tail > 0 && full == 0) {
+    int splits = slots / tail;
+    if (splits > kblocks / 4) splits = kblocks / 4;
+    if (splits > 1) {
+      p.full_tiles = 0;
+      p.tail_splits = splits;
+      p.units = tail * splits;
+    }
+  }
+  return p;
 }
 
 template <class C>
@@ -264,6 +328,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
       tmem_relinquish();
     }
   }
+  // the offsets are an input of the call, complete like the tokens
+  if constexpr (C::GROUPED)
+    if (warp == 7) build_group_table(args.groups, C::TILE_COLS, group_table(smem + C::OFF_GROUPS));
   tc_fence_before();
   __syncthreads();
   // a pair: both CTAs' barriers are initialised (and their TMEM allocated)
@@ -302,11 +369,66 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
   // (number of pairs)-th tile
   const int row_tiles = (args.rows + C::TILE_ROWS - 1) / C::TILE_ROWS;
   const int col_tiles = (args.cols + C::TILE_COLS - 1) / C::TILE_COLS;
-  const int num_tiles = args.full_tiles + (row_tiles * col_tiles - args.full_tiles) *
-                                             (args.tail_subtiles > 1 ? args.tail_subtiles : args.tail_splits);
   const int first_tile = static_cast<int>(blockIdx.x) / C::NCTA;
   const int tile_step = static_cast<int>(gridDim.x) / C::NCTA;
-  auto coord = [&](int tile) { return tile_coord(args, tile, row_tiles, col_tiles, C::TILE_COLS, C::NCTA, rank); };
+  const GroupTable gt = group_table(smem + C::OFF_GROUPS);  // GROUPED only
+  GroupedPlan gp{};
+  if constexpr (C::GROUPED)
+    gp = plan_grouped(row_tiles * gt.cum[args.groups.groups], tile_step, args.kblocks, C::NTT);
+  const int num_tiles = C::GROUPED ? gp.units
+                                   : args.full_tiles + (row_tiles * col_tiles - args.full_tiles) *
+                                         (args.tail_subtiles > 1 ? args.tail_subtiles : args.tail_splits);
+  auto coord = [&](int unit) -> TileCoord {
+    if constexpr (!C::GROUPED) {
+      TileCoord t = tile_coord(args, unit, row_tiles, col_tiles, C::TILE_COLS, C::NCTA, rank);
+      t.group = 0;
+      t.end = args.cols;
+      t.nst = C::NTT;
+      t.half = C::B_ROWS;
+      return t;
+    } else {
+      TileCoord t;
+      int id = unit;
+      t.only = -1;
+      t.split = 0;
+      t.nsplit = 1;
+      t.tail = -1;
+      if (unit >= gp.full_tiles) {
+        const int v = unit - gp.full_tiles, parts = gp.tail_subtiles > 1 ? gp.tail_subtiles : gp.tail_splits;
+        t.tail = v / parts;
+        id = gp.full_tiles + t.tail;
+        if (gp.tail_subtiles > 1) {
+          t.only = v - t.tail * parts;
+        } else {
+          t.split = v - t.tail * parts;
+          t.nsplit = parts;
+        }
+      }
+      const int g = group_of_tile(gt, args.groups.groups, id / row_tiles);
+      const int ct_n = gt.cum[g + 1] - gt.cum[g];
+      const int local = id - row_tiles * gt.cum[g];
+      const int rt = local / ct_n, ct = local - rt * ct_n;
+      t.group = g;
+      t.row0 = (rt * C::NCTA + static_cast<int>(rank)) * 128;
+      t.col0 = gt.first[g] + ct * C::TILE_COLS;
+      const int left = gt.first[g + 1] - t.col0;
+      const int ntok = left < C::TILE_COLS ? left : C::TILE_COLS;
+      t.end = t.col0 + ntok;
+      t.nst = ntok > C::BN ? 2 : 1;  // (NTT = 1: never over BN)
+      // columns per sub-tile: a multiple of 64, so that a 32-column chunk of
+      // the epilogue lies in one CTA half
+      t.half = (((ntok + t.nst - 1) / t.nst + 63) / 64) * 32;
+      t.rc = t.tail * C::NCTA + static_cast<int>(rank);  // counter of a split tile
+      t.kb_begin = static_cast<int>((static_cast<int64_t>(t.split) * args.kblocks) / t.nsplit);
+      t.nmain = static_cast<int>((static_cast<int64_t>(t.split + 1) * args.kblocks) / t.nsplit) - t.kb_begin;
+      t.nlora = t.split == t.nsplit - 1 ? args.lora_kblocks : 0;
+      if (t.only >= t.nst) {  // the tile has one sub-tile and another unit computes it
+        t.nmain = 0;
+        t.nlora = 0;
+      }
+      return t;
+    }
+  };
 
   if (warp == 4) {
     // --------------------------------- TMA: token stages, low-rank operands --
@@ -328,6 +450,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
       };
       for (int tile = first_tile; ok && tile < num_tiles; tile += tile_step) {
         const TileCoord t = coord(tile);
+        // first token that this CTA loads: its half of every sub-tile, consecutive
+        const int tok = t.col0 + static_cast<int>(rank) * (C::GROUPED ? t.nst * t.half : C::CTA_TOK);
         const int nbm = (t.nmain + C::BKB - 1) / C::BKB;
         for (int st = 0; st < nbm + t.nlora; ++st, ++bs) {
           const int sb = bs % C::SB;
@@ -337,7 +461,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
             // BKB K blocks of this CTA's tokens, one 3-D box
             if (rank == 0) mbar_arrive_expect_tx(b_full(sb), C::MAIN_TX);
             const int kb = t.kb_begin + st * C::BKB;
-            const int tok = t.col0 + static_cast<int>(rank) * C::CTA_TOK;
             if constexpr (C::PAIR) tma_load_3d_pair(b_dst, &args.tm_b, map_cluster(b_full(sb), 0u), 0, tok, kb);
             else tma_load_3d(b_dst, &args.tm_b, b_full(sb), 0, tok, kb);
             job += (st + 1 < nbm) ? C::BKB : t.nmain - st * C::BKB;
@@ -349,8 +472,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
             if (!mbar_wait(a_empty(sa), ((job / C::SA) & 1u) ^ 1u, s_abort)) { ok = false; break; }
             const uint32_t a_dst = sbase + C::OFF_A + sa * C::A_BYTES;
             if (rank == 0) mbar_arrive_expect_tx(b_full(sb), C::LORA_TX);
-            load(b_dst, &args.tm_b2, b_full(sb), lk * 64, t.col0 + static_cast<int>(rank) * C::CTA_TOK);
-            if (C::L2 == L2_A_MN) {
+            load(b_dst, &args.tm_b2, b_full(sb), lk * 64, tok);
+            if constexpr (C::GROUPED) {
+              // this expert's adapter, one slice of a 3-D map: ranks past r read as zeros, not as the next expert's
+              const uint32_t bar = map_cluster(b_full(sb), 0u);
+              if (C::L2 == L2_A_MN) {
+                tma_load_3d_pair(a_dst, &args.tm_a2, bar, t.row0, lk * 64, t.group);
+                tma_load_3d_pair(a_dst + 8192, &args.tm_a2, bar, t.row0 + 64, lk * 64, t.group);
+              } else {
+                tma_load_3d_pair(a_dst, &args.tm_a2, bar, lk * 64, t.row0, t.group);
+              }
+            } else if (C::L2 == L2_A_MN) {
               load(a_dst, &args.tm_a2, b_full(sb), t.row0, lk * 64);
               load(a_dst + 8192, &args.tm_a2, b_full(sb), t.row0 + 64, lk * 64);
             } else {
@@ -387,9 +519,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
     if (lane == 0 && rank == 0) {
       constexpr uint64_t DK = smem_desc_const(16, 1024);    // K-major, 128B swizzle
       constexpr uint64_t DM = smem_desc_const(8192, 1024);  // MN-major, 128B swizzle
-      const uint32_t ID_MAIN = idesc_dtype(make_idesc_bf16(C::TILE_ROWS, C::BN, C::A_MN ? 1 : 0, 0), args.f16);
-      const uint32_t ID_LORA =
-          idesc_dtype(make_idesc_bf16(C::TILE_ROWS, C::BN, C::L2 == L2_A_MN ? 1 : 0, 0), args.f16);
+      constexpr int IDN = C::GROUPED ? 0 : C::BN;  // grouped: the columns of each tile
+      const uint32_t ID_MAIN = idesc_dtype(make_idesc_bf16(C::TILE_ROWS, IDN, C::A_MN ? 1 : 0, 0), args.f16);
+      const uint32_t ID_LORA = idesc_dtype(make_idesc_bf16(C::TILE_ROWS, IDN, C::L2 == L2_A_MN ? 1 : 0, 0), args.f16);
       auto wait_full = [&](uint32_t bar, uint32_t par) -> bool {
         return mbar_try_wait(bar, par) || mbar_wait(bar, par, s_abort);
       };
@@ -407,8 +539,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
       for (int tile = first_tile; ok && tile < num_tiles; tile += tile_step, ++iter) {
         const TileCoord t = coord(tile);
         const int njobs = t.nmain + t.nlora;
-        // accumulator use u = iter * NTT + sub-tile: accumulator u & 1, phase u >> 1
-        const uint32_t u0 = iter * C::NTT;
+        if (C::GROUPED && njobs == 0) {  // nothing to do and no accumulator used
+          --iter;
+          continue;
+        }
+        // accumulator use u = iter * USES + sub-tile: accumulator u & 1, phase u >> 1
+        const uint32_t u0 = iter * C::USES;
+        const int half = C::GROUPED ? t.half : C::B_ROWS;
+        const uint32_t ncols = C::GROUPED ? static_cast<uint32_t>(2 * t.half) >> 3 << 17 : 0u;  // MMA N field
         int sa = job % C::SA;
         uint32_t pa = (job / C::SA) & 1u;
         for (int jj = 0; jj < njobs; ++jj, ++job) {
@@ -423,7 +561,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
           const uint64_t ad = (a_mn ? DM : DK) | (((a_base + sa * C::A_BYTES) >> 4) & 0x3FFFu);
           const uint64_t bd = DK | (((b_base + sb * C::B_BYTES + sub * C::KB_BYTES) >> 4) & 0x3FFFu);
           const uint32_t astep = a_mn ? 2048u >> 4 : 32u >> 4, bstep = 32u >> 4;
-          const uint32_t idesc = main_job ? ID_MAIN : ID_LORA;
+          const uint32_t idesc = (main_job ? ID_MAIN : ID_LORA) | ncols;
 #pragma unroll
           for (int st = 0; st < C::NTT; ++st) {
             const uint32_t u = u0 + st;
@@ -431,15 +569,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
               if (!wait_full(tmem_empty(u & 1u), ((u >> 1) & 1u) ^ 1u)) { ok = false; break; }
               tc_fence_after();
             }
-            if (t.only >= 0 && st != t.only) {
-              // a sub-tile this unit leaves to another: its accumulator's
-              // phases still advance (nothing to drain, nothing written)
+            if ((t.only >= 0 && st != t.only) || (C::GROUPED && st >= t.nst)) {
+              // a sub-tile this unit leaves to another, or without tokens: its
+              // accumulator's phases still advance (nothing to drain, nothing written)
               if (jj == njobs - 1) commit(tmem_full(u & 1u));
               continue;
             }
-            const uint32_t d_tmem = tmem_base + (u & 1u) * C::ACC_STRIDE;
-            const uint64_t bst = bd + ((st * C::B_ROWS * 128) >> 4);  // sub-tile st's tokens of the stage
-            mma(d_tmem, ad, bst, idesc, jj > 0 ? 1u : 0u);
+            const bool sep = C::SEP && !main_job;  // the low-rank sum's own accumulator
+            const uint32_t d_tmem = tmem_base + (sep ? 1u : u & 1u) * C::ACC_STRIDE;
+            const uint64_t bst = bd + ((st * half * 128) >> 4);  // sub-tile st's tokens of the stage
+            mma(d_tmem, ad, bst, idesc, jj > (sep ? t.nmain : 0) ? 1u : 0u);
             mma(d_tmem, ad + astep, bst + bstep, idesc, 1u);
             mma(d_tmem, ad + 2 * astep, bst + 2 * bstep, idesc, 1u);
             mma(d_tmem, ad + 3 * astep, bst + 3 * bstep, idesc, 1u);
@@ -455,11 +594,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
         }
       }
       // all MMAs issued by this thread have completed once drain_bar flips
-      if constexpr (C::PAIR) tc_commit_pair(drain_bar, 0x1);
-      else tc_commit(drain_bar);
-      const unsigned long long t0 = globaltimer_ns();
-      while (!mbar_try_wait(drain_bar, 0)) {
-        if (globaltimer_ns() - t0 > kWaitTimeoutNs) break;
+      // (a grouped launch may leave a pair without units)
+      if (!C::GROUPED || job > 0) {
+        if constexpr (C::PAIR) tc_commit_pair(drain_bar, 0x1);
+        else tc_commit(drain_bar);
+        const unsigned long long t0 = globaltimer_ns();
+        while (!mbar_try_wait(drain_bar, 0)) {
+          if (globaltimer_ns() - t0 > kWaitTimeoutNs) break;
+        }
       }
     }
     __syncwarp();
@@ -473,7 +615,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
     volatile int *s_last = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8);
     // partial rows are padded to whole 32-column chunks per sub-tile
     constexpr int TILE_PCOLS = C::NTT * C::NCHUNK * 32;
-    const int ntail = row_tiles * col_tiles - args.full_tiles;
+    const int ntail = C::GROUPED ? gp.tiles - gp.full_tiles : row_tiles * col_tiles - args.full_tiles;
     // Partial of split sp of tail tile ti, column-major ([column][row]) so
     // that the 32 threads of a warp (32 consecutive rows) store and load 128
     // contiguous bytes: this thread's element of column c is part_col(..)[c * TILE_ROWS].
@@ -497,11 +639,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
         tmem_ld_32x32b_x32(tcol + ch * 32, u);
       }
     };
-    // out[token][row] for the 32 consecutive tokens from tok (clipped at the
-    // last token); each warp store covers 32 consecutive rows
-    auto store_out = [&](int row, int tok, const float (&v)[32]) {
+    // out[token][row] for the 32 consecutive tokens from tok (clipped at
+    // `end`); each warp store covers 32 consecutive rows
+    auto store_out = [&](int row, int tok, int end, const float (&v)[32]) {
       if (row >= args.rows) return;
-      const int ncol = args.cols - tok < 32 ? args.cols - tok : 32;
+      const int ncol = end - tok < 32 ? end - tok : 32;
       uint16_t *dst = reinterpret_cast<uint16_t *>(args.out);
       const bool f16 = args.f16 != 0;
 #pragma unroll
@@ -511,19 +653,48 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
     bool ok = true;
     for (int tile = first_tile; ok && tile < num_tiles; tile += tile_step, ++iter) {
       const TileCoord t = coord(tile);
+      if (C::GROUPED && t.nmain == 0) {
+        --iter;
+        continue;
+      }
       const int row = t.row0 + qrow;
+      const int end = C::GROUPED ? t.end : args.cols;
+      const int nchunk = C::GROUPED ? t.half / 16 : C::NCHUNK;  // chunks with columns, per sub-tile
+      const int nsub = C::GROUPED ? t.nst : C::NTT;
       // first token of chunk ch of sub-tile st (32 columns never straddle the CTA halves)
       auto tok0 = [&](int st, int ch) {
         const int c0 = ch * 32;
-        return t.col0 + (c0 / C::B_ROWS) * C::CTA_TOK + st * C::B_ROWS + c0 % C::B_ROWS;
+        if constexpr (C::GROUPED) {
+          const int hi = c0 >= t.half ? 1 : 0;
+          return t.col0 + hi * t.nst * t.half + st * t.half + c0 - hi * t.half;
+        } else {
+          return t.col0 + (c0 / C::B_ROWS) * C::CTA_TOK + st * C::B_ROWS + c0 % C::B_ROWS;
+        }
       };
+      // SEP: keep bits of the 32 rows of this warp for token tok0(0, ch) +
+      // lane, evaluated while the tile's MMAs run
+      uint32_t keep[C::SEP ? C::NCHUNK : 1];
+      if constexpr (C::SEP) {
+        const int base = t.row0 + warp * 32;  // rows is a multiple of 64: 32 rows or none
+#pragma unroll 1
+        for (int ch = 0; ch < nchunk; ++ch) {
+          const int tok = tok0(0, ch) + lane;
+          uint32_t word = 0u;
+          if (t.nlora > 0 && tok < end && base < args.rows) {
+            const uint64_t group = (static_cast<uint64_t>(tok) * args.out_ld + base) / 8;
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) word |= dropout_keep8(args.drop, group + j) << (8 * j);
+          }
+          keep[ch] = word;
+        }
+      }
       float *pcol = t.nsplit > 1 ? part_col(t.split, t.tail) : nullptr;
 #pragma unroll 1
       for (int st = 0; st < C::NTT; ++st) {
-        const uint32_t u = iter * C::NTT + st;
+        const uint32_t u = iter * C::USES + st;
         if (!wait_warp(tmem_full(u & 1u), (u >> 1) & 1u)) { ok = false; break; }
         tc_fence_after();
-        if (t.only >= 0 && st != t.only) {  // computed by another unit
+        if ((t.only >= 0 && st != t.only) || st >= nsub) {  // computed by another unit, or without tokens
           tc_fence_before();
           __syncwarp();
           if (lane == 0) arrive_leader(tmem_empty(u & 1u));
@@ -531,14 +702,27 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
         }
         const uint32_t tcol = tmem_base + ((uint32_t)(warp * 32) << 16) + (u & 1u) * C::ACC_STRIDE;
 #pragma unroll 1
-        for (int ch = 0; ch < C::NCHUNK; ++ch) {
+        for (int ch = 0; ch < nchunk; ++ch) {
           uint32_t w[32];
           load_chunk(tcol, ch, w);
+          if constexpr (C::SEP) {
+            if (t.nlora > 0) {  // join the low-rank sum, each element under its keep bit
+              uint32_t l[32];
+              tmem_ld_32x32b_x32(tcol + C::ACC_STRIDE + ch * 32, l);
+              const uint32_t word = keep[ch];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const uint32_t bits = __shfl_sync(0xFFFFFFFFu, word, j);
+                const float add = (bits >> lane) & 1u ? __uint_as_float(l[j]) * args.drop.factor : 0.0f;
+                w[j] = __float_as_uint(__uint_as_float(w[j]) + add);
+              }
+            }
+          }
           if (t.nsplit == 1) {
             float v[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]);
-            store_out(row, tok0(st, ch), v);
+            store_out(row, tok0(st, ch), end, v);
           } else {
             float *o = pcol + static_cast<int64_t>((st * C::NCHUNK + ch) * 32) * C::TILE_ROWS;
 #pragma unroll
@@ -564,6 +748,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
         __threadfence();
 #pragma unroll 1
         for (int pc = 0; pc < C::NTT * C::NCHUNK; ++pc) {
+          if (C::GROUPED && (pc / C::NCHUNK >= nsub || pc % C::NCHUNK >= nchunk)) continue;  // no columns there
           float v[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = 0.0f;
@@ -572,7 +757,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] += __ldcg(src + j * C::TILE_ROWS);
           }
-          store_out(row, tok0(pc / C::NCHUNK, pc % C::NCHUNK), v);
+          store_out(row, tok0(pc / C::NCHUNK, pc % C::NCHUNK), end, v);
         }
       }
     }
@@ -591,8 +776,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
           const int kb0 = t.kb_begin + u * C::KSUP;
           const uint32_t p_dst = sbase + C::OFF_P + sp * C::P_BYTES;
           mbar_arrive_expect_tx(p_full(sp), C::P_BYTES);
-          if (C::ASRC == A_DEQ_K) tma_load_2d(p_dst, &args.tm_pk, p_full(sp), kb0 * 32, t.row0);
-          else tma_load_2d(p_dst, &args.tm_pk, p_full(sp), t.row0 / 2, kb0 * 64);
+          const int w0 = C::GROUPED ? t.group * args.expert_rows : 0;  // the expert's first weight row
+          if (C::ASRC == A_DEQ_K) tma_load_2d(p_dst, &args.tm_pk, p_full(sp), kb0 * 32, w0 + t.row0);
+          else tma_load_2d(p_dst, &args.tm_pk, p_full(sp), t.row0 / 2, w0 + kb0 * 64);
         }
       }
       // wait (bounded) for this thread's own copies still in flight
@@ -632,6 +818,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
       qv = 0u;
       sv = 0.0f;
       if (valid) {
+        if constexpr (C::GROUPED) n += static_cast<int64_t>(t.group) * args.expert_rows;
         const int64_t b = n * args.wkb + kblk;
         qv = __ldg(args.q + b);
         sv = __ldg(args.scale2 + (b >> 8));

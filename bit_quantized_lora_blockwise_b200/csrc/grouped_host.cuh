@@ -1,0 +1,394 @@
+// Host side of the expert-grouped linear and of dropout: plans, workspace,
+// tensor maps and launch order. Included by qlora.cu inside its unnamed
+// namespace (it uses that file's launchers and map helpers).
+//
+// The host knows E and T but not the offsets, so it sizes grids and
+// workspaces for the worst split of T tokens over E experts, and picks
+// variants from the average tokens per expert; every variant is right for
+// every split.
+
+// An expert of c tokens has ceil(c / tile) token tiles: at most T / tile full
+// ones in all and one partial one per expert with tokens.
+inline int64_t token_tiles_bound(int64_t T, int64_t E, int64_t tile) {
+  return std::min(T, T / tile + std::min(E, T));
+}
+
+struct GroupedShape {
+  int64_t E, T, N, K;
+  int r;
+  bool drop;
+};
+
+// Variant choice by the average tokens per expert (T / E).
+constexpr int64_t kGroupedStreamTokens = 24;   // up to here: the register-dequant stream
+constexpr int64_t kGroupedTwoSubtile = 384;    // from here: two 256-token sub-tiles per tile
+
+using GroupedFwd1 = GemmCfg<256, A_DEQ_K, L2_A_MN, kPairBkb, kPairSb, kPairSa, kPairSp, kPairNpw, true, 1, true>;
+using GroupedFwd2 = GemmCfg<256, A_DEQ_K, L2_A_MN, kPair2Bkb, kPair2Sb, kPair2Sa, kPair2Sp, kPair2Npw, true, 2, true>;
+using GroupedBwd1 = GemmCfg<256, A_DEQ_MN, L2_A_K, kPairBkb, kPairSb, kPairSa, kPairSp, kPairNpw, true, 1, true>;
+using GroupedBwd2 = GemmCfg<256, A_DEQ_MN, L2_A_K, kPair2Bkb, kPair2Sb, kPair2Sa, kPair2Sp, kPair2Npw, true, 2, true>;
+using GroupedBwdDrop =
+    GemmCfg<256, A_DEQ_MN, L2_A_K, kPairBkb, kPairSb, kPairSa, kPairSp, kPairNpw, true, 1, true, true>;
+
+int grouped_pair_slots(int sms) {
+  const int n = std::min({resident_pairs<GroupedFwd1>(), resident_pairs<GroupedFwd2>(), resident_pairs<GroupedBwd1>(),
+                          resident_pairs<GroupedBwd2>(), resident_pairs<GroupedBwdDrop>()});
+  return std::min(n, sms / 2);  // 0 without a device: the calls then return before any launch
+}
+
+struct GroupedFwdPlan {
+  bool stream;
+  int nt, kc, grid;  // stream: 8 nt tokens per pass
+  int64_t bands, counters;
+  int ntt, slots;    // GEMM
+  size_t part;
+};
+
+// Partials of a grouped GEMM split over K: splits x tiles <= slots (plan_grouped).
+size_t grouped_part_bytes(int slots, int ntt, int64_t kblocks) {
+  return kblocks / 4 >= 2 ? align256(static_cast<size_t>(slots) * 256 * ntt * 256 * 4) : 0;
+}
+
+GroupedFwdPlan plan_grouped_fwd(const GroupedShape &s, int sms) {
+  GroupedFwdPlan p{};
+  const int64_t avg = s.T / s.E;
+  p.bands = cdiv(s.N, SmallmCfg<1>::BAND);
+  p.kc = static_cast<int>(cdiv(s.K, 256));
+  p.nt = s.T <= 8 ? 1 : (s.T <= 16 || avg <= 4 ? 2 : 4);
+  const int64_t tiles = token_tiles_bound(s.T, s.E, 8 * p.nt);
+  p.stream = avg <= kGroupedStreamTokens && tiles * p.bands * p.kc < (int64_t(1) << 30);
+  if (p.stream) {
+    p.grid = static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, tiles * p.bands * p.kc / 2), sms));
+    p.counters = tiles * p.bands;
+    p.part = align256(static_cast<size_t>(p.grid) * 2 * SmallmCfg<1>::WARPS * p.nt * 32 * 16);
+  } else {
+    p.ntt = avg >= kGroupedTwoSubtile ? 2 : 1;
+    p.slots = grouped_pair_slots(sms);
+    p.counters = 2 * p.slots;
+    p.part = grouped_part_bytes(p.slots, p.ntt, s.K / 64);
+  }
+  return p;
+}
+
+struct GroupedBwdPlan {
+  int ntt, slots;
+  int64_t counters;
+  size_t part;
+};
+GroupedBwdPlan plan_grouped_bwd(const GroupedShape &s, int sms) {
+  GroupedBwdPlan p{};
+  p.ntt = !s.drop && s.T / s.E >= kGroupedTwoSubtile ? 2 : 1;
+  p.slots = grouped_pair_slots(sms);
+  p.counters = 2 * p.slots;
+  p.part = grouped_part_bytes(p.slots, p.ntt, s.N / 64);
+  return p;
+}
+
+// [counters][16-bit T x r][16-bit T x r (backward)][16-bit T x K: M o X, with dropout][fp32 partials]
+struct GroupedWs {
+  size_t counters, tr, xm, part, total;
+};
+GroupedWs grouped_ws(const GroupedShape &s, int64_t ncounters, size_t part, bool backward) {
+  GroupedWs w;
+  w.counters = align256(static_cast<size_t>(ncounters) * 4);
+  w.tr = align256(static_cast<size_t>(s.T) * s.r * 2);
+  w.xm = s.drop ? align256(static_cast<size_t>(s.T) * s.K * 2) : 0;
+  w.part = part;
+  w.total = w.counters + (backward ? 2 : 1) * w.tr + w.xm + w.part;
+  return w;
+}
+
+// Shapes that every grouped kernel can index: weight rows, tile and unit
+// counts stay within int32.
+qlora_status check_grouped(const GroupedShape &s) {
+  if (s.E < 1 || s.E > QLORA_MAX_EXPERTS || s.T < 0 || s.N < 64 || s.K < 64 || s.N % 64 || s.K % 64)
+    return QLORA_ERR_SHAPE;
+  const int64_t lim = int64_t(1) << 30;
+  if (s.T > lim || s.N > lim || s.K > lim || s.E * s.N > lim || s.E * s.K > lim) return QLORA_ERR_SHAPE;
+  if (token_tiles_bound(s.T, s.E, 256) * cdiv(std::max(s.N, s.K), 128) * 8 > lim) return QLORA_ERR_SHAPE;
+  if (s.r < 1 || s.r > QLORA_MAX_RANK || s.r % 8) return QLORA_ERR_RANGE;
+  return QLORA_OK;
+}
+
+// Threshold and factor of a dropout description (dropout.cuh); NULL or a
+// threshold of 0 drops nothing.
+qlora_status make_dropout(const qlora_dropout_desc *d, DropoutArgs *out) {
+  *out = DropoutArgs{0, 0, 0u, 1.0f};
+  if (d == nullptr) return QLORA_OK;
+  if (!(d->p >= 0.0 && d->p < 1.0)) return QLORA_ERR_RANGE;
+  const double t = std::floor(d->p * 65536.0 + 0.5);
+  if (t > 65535.0) return QLORA_ERR_RANGE;
+  out->seed = d->seed;
+  out->offset = d->offset;
+  out->threshold = static_cast<uint32_t>(t);
+  out->factor = static_cast<float>(65536.0 / (65536.0 - t));
+  return QLORA_OK;
+}
+
+// One thread per 8 elements, at most eight CTAs per SM in one wave.
+qlora_status run_dropout(const void *x, void *y, int64_t n, int type, const DropoutArgs &d, float factor, int sms,
+                         cudaStream_t st) {
+  const int grid = grid_for(cdiv(n, 8), 256, sms, 8);
+  if (type == DROP_F32) return launch_pdl(dropout_kernel<DROP_F32>, grid, 256, 0, st, x, y, n, d, factor);
+  if (type == DROP_F16) return launch_pdl(dropout_kernel<DROP_F16>, grid, 256, 0, st, x, y, n, d, factor);
+  return launch_pdl(dropout_kernel<DROP_BF16>, grid, 256, 0, st, x, y, n, d, factor);
+}
+
+// Expert stack of 16-bit matrices [groups][outer][inner]: box {box_inner, box_outer, 1}.
+bool map_experts_3d(CUtensorMap *map, const void *p, int64_t inner, int64_t outer, int64_t groups, uint32_t box_inner,
+                    uint32_t box_outer) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
+                              static_cast<cuuint64_t>(groups)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(inner) * 2, static_cast<cuuint64_t>(inner * outer) * 2};
+  const cuuint32_t box[3] = {box_inner, box_outer, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// out[T, r] = scale * rows . adapter_e: X A (kind SK_XA) or dY B^T (SK_G),
+// optionally a second copy with another scale.
+qlora_status grouped_rows(SkinnyKind kind, const void *rows, const void *adapter, const GroupedShape &s,
+                          const GroupArgs &g, void *out, float scale, void *out2, float scale2,
+                          unsigned int *zero_words, int64_t nzero, cudaStream_t st) {
+  const int64_t kdim = kind == SK_XA ? s.K : s.N;
+  const int64_t tiles = token_tiles_bound(s.T, s.E, 128);
+  SkinnyPlan p;
+  qlora_status e = kind == SK_XA ? plan_skinny_v<false, true, true>(tiles * 128, kdim, s.r, &p)
+                                 : plan_skinny_v<false, false, true>(tiles * 128, kdim, s.r, &p);
+  if (e != QLORA_OK) return e;
+  SkinnyArgs a;
+  std::memset(&a, 0, sizeof a);
+  SkinnyProblem &P = a.prob[0];
+  const bool ok = map_kmajor(&P.tm_a, rows, kdim, s.T, 128) &&
+                  (kind == SK_XA ? map_experts_3d(&P.tm_b, adapter, s.r, s.K, s.E, 64, 64)
+                                 : map_experts_3d(&P.tm_b, adapter, s.N, s.r, s.E, 64, static_cast<uint32_t>(p.bn)));
+  if (!ok) return QLORA_ERR_CUDA;
+  P.out = out;
+  P.out_ld = s.r;
+  P.out_scale = scale;
+  P.out2 = out2;
+  P.out2_ld = s.r;
+  P.out2_scale = scale2;
+  P.rows = static_cast<int>(s.T);
+  P.cols = s.r;
+  P.kblocks = static_cast<int>(kdim / 64);
+  a.splits = p.splits;
+  const int grid = static_cast<int>(tiles) * p.splits;
+  a.prob0_ctas = grid;
+  a.zero_words = zero_words;
+  a.nzero = static_cast<int>(nzero);
+  a.f16 = t_f16 ? 1 : 0;
+  a.groups = g;
+  return kind == SK_XA ? run_skinny<false, true, true>(a, p.bn, grid, st)
+                       : run_skinny<false, false, true>(a, p.bn, grid, st);
+}
+
+// dA_e = factor * xm_e^T gs_e and dB_e = (xa_e^T dY_e) * s, every expert's in one launch.
+qlora_status grouped_adapter_grads(const void *xm, const void *dY, const void *gs, const void *xa, const GroupedShape &s,
+                                   const GroupArgs &g, void *dA, float a_scale, void *dB, float b_scale,
+                                   cudaStream_t st) {
+  const int64_t ta = s.E * cdiv(s.K, 128), tb = s.E * cdiv(s.N, 128);
+  SkinnyPlan p;
+  const qlora_status e = plan_skinny_v<true, true, true>((ta + tb) * 128, cdiv(s.T, s.E), s.r, &p);
+  if (e != QLORA_OK) return e;
+  SkinnyArgs a;
+  std::memset(&a, 0, sizeof a);
+  SkinnyProblem &A = a.prob[0], &B = a.prob[1];
+  if (!map_mnmajor(&A.tm_a, xm, s.K, s.T) || !map_mnmajor(&A.tm_b, gs, s.r, s.T) ||
+      !map_mnmajor(&B.tm_a, dY, s.N, s.T) || !map_mnmajor(&B.tm_b, xa, s.r, s.T))
+    return QLORA_ERR_CUDA;
+  A.out = dA;
+  A.out_ld = s.r;
+  A.out_scale = a_scale;
+  A.rows = static_cast<int>(s.K);
+  A.cols = s.r;
+  B.out = dB;
+  B.out_ld = s.N;
+  B.out_scale = b_scale;
+  B.transpose = 1;
+  B.rows = static_cast<int>(s.N);
+  B.cols = s.r;
+  a.splits = p.splits;
+  a.prob0_ctas = static_cast<int>(ta) * p.splits;
+  a.late = 1;
+  a.f16 = t_f16 ? 1 : 0;
+  a.groups = g;
+  return run_skinny<true, true, true>(a, p.bn, static_cast<int>(ta + tb) * p.splits, st);
+}
+
+template <class C>
+qlora_status run_grouped_gemm(const GemmArgs &args, int slots, cudaStream_t stream) {
+  if (slots < 1) return QLORA_ERR_CUDA;  // (resident_pairs has set the kernel's shared memory)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * slots);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, qgemm_kernel<C>, args);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
+  return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+// What forward and backward share of the GEMM's arguments.
+void grouped_gemm_args(GemmArgs *a, const uint8_t *q, const float *scale2, const float *nf4, const float *t8,
+                       const GroupedShape &s, const GroupArgs &g, int64_t rows, int64_t kblocks, void *out, float *part,
+                       unsigned int *counters) {
+  a->rows = static_cast<int>(rows);
+  a->cols = static_cast<int>(s.T);
+  a->kblocks = static_cast<int>(kblocks);
+  a->lora_kblocks = static_cast<int>(cdiv(s.r, 64));
+  a->out = out;
+  a->out_ld = rows;
+  a->part = part;
+  a->counters = counters;
+  std::memcpy(a->nf4, nf4, sizeof a->nf4);
+  std::memcpy(a->t8, t8, sizeof a->t8);
+  a->q = q;
+  a->scale2 = scale2;
+  a->wkb = s.K / 64;
+  a->f16 = t_f16 ? 1 : 0;
+  a->groups = g;
+  a->expert_rows = static_cast<int>(s.N);
+}
+
+qlora_status grouped_fwd(const uint8_t *packed, const uint8_t *q, const float *scale2, const float *nf4,
+                         const float *t8, const GroupedShape &s, const int *offsets, const void *X, const void *A,
+                         const void *B, float alpha, const DropoutArgs &drop, void *Y, void *XA_out, void *workspace,
+                         size_t workspace_bytes, int sms, cudaStream_t cs) {
+  const GroupedFwdPlan p = plan_grouped_fwd(s, sms);
+  const GroupedWs w = grouped_ws(s, p.counters, p.part, false);
+  if (!workspace || workspace_bytes < w.total) return QLORA_ERR_WORKSPACE;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  unsigned int *counters = reinterpret_cast<unsigned int *>(ws);
+  void *xas = ws + w.counters;
+  void *xm = ws + w.counters + w.tr;
+  float *part = reinterpret_cast<float *>(ws + w.counters + w.tr + w.xm);
+  const GroupArgs g{offsets, static_cast<int>(s.E), static_cast<int>(s.T)};
+  const float scl = alpha / static_cast<float>(s.r);
+  qlora_status st = QLORA_OK;
+
+  // 1) the adapter branch's input: M o X (kept elements as they are: exact;
+  //    the factor 1 / (1 - p) goes into the fp32 scales below)
+  const void *xin = X;
+  if (s.drop) {
+    st = run_dropout(X, xm, s.T * s.K, t_f16 ? DROP_F16 : DROP_BF16, drop, 1.0f, sms, cs);
+    if (st != QLORA_OK) return st;
+    xin = xm;
+  }
+  // 2) XA, and s XA for the low-rank step; zeroes the counters
+  st = grouped_rows(SK_XA, xin, A, s, g, xas, scl * drop.factor, XA_out, drop.factor, counters, p.counters, cs);
+  if (st != QLORA_OK) return st;
+
+  // 3) the base product, whose main loop overlaps 2)
+  if (p.stream) {
+    SmallmArgs a;
+    std::memset(&a, 0, sizeof a);
+    if (!map_x_blocks(&a.tm_x, X, s.T, s.K, static_cast<uint32_t>(8 * p.nt)) ||
+        !make_map(&a.tm_w, packed, MAP_U8, s.K / 2, s.E * s.N, s.K / 2, 128, SmallmCfg<1>::BAND, SW_128B))
+      return QLORA_ERR_CUDA;
+    a.q = q;
+    a.scale2 = scale2;
+    a.B = static_cast<const uint16_t *>(B);
+    a.xas = static_cast<const uint16_t *>(xas);
+    a.Y = static_cast<uint16_t *>(Y);
+    a.part = part;
+    a.counters = counters;
+    a.N = s.N;
+    a.K = s.K;
+    a.M = static_cast<int>(s.T);
+    a.r = s.r;
+    a.kc = p.kc;
+    a.tabs = make_tables(nf4, t8);
+    a.groups = g;
+    trace_begin(cs);
+    if (t_f16)
+      st = p.nt == 1 ? run_smallm_nt<1, true, true>(a, p.grid, cs)
+                     : p.nt == 2 ? run_smallm_nt<2, true, true>(a, p.grid, cs) : run_smallm_nt<4, true, true>(a, p.grid, cs);
+    else
+      st = p.nt == 1 ? run_smallm_nt<1, false, true>(a, p.grid, cs)
+                     : p.nt == 2 ? run_smallm_nt<2, false, true>(a, p.grid, cs) : run_smallm_nt<4, false, true>(a, p.grid, cs);
+    trace_end(cs);
+    return st;
+  }
+  GemmArgs a;
+  std::memset(&a, 0, sizeof a);
+  const uint32_t box = static_cast<uint32_t>(128 * p.ntt);
+  if (!map_tokens_3d(&a.tm_b, X, s.T, s.K, box, 1) ||
+      !make_map(&a.tm_pk, packed, MAP_U8, s.K / 2, s.E * s.N, s.K / 2, 128, 128, SW_128B) ||
+      !map_experts_3d(&a.tm_a2, B, s.N, s.r, s.E, 64, 64) || !map_kmajor(&a.tm_b2, xas, s.r, s.T, box))
+    return QLORA_ERR_CUDA;
+  grouped_gemm_args(&a, q, scale2, nf4, t8, s, g, s.N, s.K / 64, Y, part, counters);
+  trace_begin(cs);
+  st = p.ntt == 2 ? run_grouped_gemm<GroupedFwd2>(a, p.slots, cs) : run_grouped_gemm<GroupedFwd1>(a, p.slots, cs);
+  trace_end(cs);
+  return st;
+}
+
+qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *scale2, const float *nf4,
+                         const float *t8, const GroupedShape &s, const int *offsets, const void *X, const void *dY,
+                         const void *A, const void *B, const void *XA, float alpha, const DropoutArgs &drop, void *dX,
+                         void *dA, void *dB, void *workspace, size_t workspace_bytes, int sms, cudaStream_t cs) {
+  const GroupedBwdPlan p = plan_grouped_bwd(s, sms);
+  const GroupedWs w = grouped_ws(s, p.counters, p.part, true);
+  if (!workspace || workspace_bytes < w.total) return QLORA_ERR_WORKSPACE;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  unsigned int *counters = reinterpret_cast<unsigned int *>(ws);
+  void *gs = ws + w.counters;
+  void *xa_ws = ws + w.counters + w.tr;
+  void *xm = ws + w.counters + 2 * w.tr;
+  float *part = reinterpret_cast<float *>(ws + w.counters + 2 * w.tr + w.xm);
+  const GroupArgs g{offsets, static_cast<int>(s.E), static_cast<int>(s.T)};
+  const float scl = alpha / static_cast<float>(s.r);
+  qlora_status st = QLORA_OK;
+
+  // 1) M o X again (never kept from the forward), XA where it was not saved,
+  //    and Gs = s dY B^T, whose launch zeroes the counters
+  const void *xin = X;
+  if (s.drop) {
+    st = run_dropout(X, xm, s.T * s.K, t_f16 ? DROP_F16 : DROP_BF16, drop, 1.0f, sms, cs);
+    if (st != QLORA_OK) return st;
+    xin = xm;
+  }
+  if (XA == nullptr) {
+    st = grouped_rows(SK_XA, xin, A, s, g, xa_ws, drop.factor, nullptr, 0.0f, nullptr, 0, cs);
+    if (st != QLORA_OK) return st;
+    XA = xa_ws;
+  }
+  st = grouped_rows(SK_G, dY, B, s, g, gs, scl, nullptr, 0.0f, counters, p.counters, cs);
+  if (st != QLORA_OK) return st;
+
+  // 2) dX
+  GemmArgs a;
+  std::memset(&a, 0, sizeof a);
+  const uint32_t box = static_cast<uint32_t>(128 * p.ntt);
+  if (!map_tokens_3d(&a.tm_b, dY, s.T, s.N, box, 1) ||
+      !make_map(&a.tm_pk, packed, MAP_U8, s.K / 2, s.E * s.N, s.K / 2, 64, 256, SW_64B) ||
+      !map_experts_3d(&a.tm_a2, A, s.r, s.K, s.E, 64, 128) || !map_kmajor(&a.tm_b2, gs, s.r, s.T, box))
+    return QLORA_ERR_CUDA;
+  grouped_gemm_args(&a, q, scale2, nf4, t8, s, g, s.K, s.N / 64, dX, part, counters);
+  a.drop = drop;
+  trace_begin(cs);
+  st = s.drop       ? run_grouped_gemm<GroupedBwdDrop>(a, p.slots, cs)
+       : p.ntt == 2 ? run_grouped_gemm<GroupedBwd2>(a, p.slots, cs)
+                    : run_grouped_gemm<GroupedBwd1>(a, p.slots, cs);
+  trace_end(cs);
+  if (st != QLORA_OK) return st;
+
+  // 3) dA and dB "late", as in the dense backward: every operand is complete
+  //    when this launch starts and dX is neither read nor written by it
+  return grouped_adapter_grads(xin, dY, gs, XA, s, g, dA, drop.factor, dB, scl, cs);
+}

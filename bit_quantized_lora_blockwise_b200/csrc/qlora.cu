@@ -11,6 +11,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <new>
 #include <vector>
@@ -20,6 +21,8 @@
 #include "gemm.cuh"
 #include "skinny.cuh"
 #include "smallm.cuh"
+#include "dropout.cuh"
+#include "groups.cuh"
 #include "adamw.cuh"
 #include "ptx.cuh"
 
@@ -447,9 +450,9 @@ constexpr int skinny_stages(int bn) { return bn == 64 ? 4 : (bn == 128 ? 3 : 4);
 // One skinny-GEMM variant: its shared-memory opt-in and how many clusters
 // of 2, 4 and 8 CTAs can be resident at once (asked of the runtime once per
 // device).
-template <int BN, bool AMN, bool BMN>
+template <int BN, bool AMN, bool BMN, bool GROUPED = false>
 struct SkinnyVariant {
-  using C = SkinnyCfg<BN, AMN, BMN, skinny_stages(BN)>;
+  using C = SkinnyCfg<BN, AMN, BMN, skinny_stages(BN), GROUPED>;
   static qlora_status prepare(int (&max_clusters)[4], int *per_sm) {
     static std::once_flag once[kMaxDevices];
     static cudaError_t err[kMaxDevices];
@@ -507,15 +510,15 @@ struct SkinnyPlan {
 // Split K over a cluster of 2, 4 or 8 CTAs per 128-row tile: the largest
 // split whose clusters for all row tiles are resident at once (one wave),
 // else one CTA per tile.
-template <bool AMN, bool BMN>
+template <bool AMN, bool BMN, bool GROUPED = false>
 qlora_status plan_skinny_v(int64_t rows, int64_t kdim, int r, SkinnyPlan *p) {
   p->rows = static_cast<int>(rows);
   p->kblocks = static_cast<int>(cdiv(kdim, 64));
   p->bn = rank_tile(r);
   int maxc[4];
-  const qlora_status st = p->bn == 64    ? SkinnyVariant<64, AMN, BMN>::prepare(maxc, &p->per_sm)
-                          : p->bn == 128 ? SkinnyVariant<128, AMN, BMN>::prepare(maxc, &p->per_sm)
-                                         : SkinnyVariant<256, AMN, BMN>::prepare(maxc, &p->per_sm);
+  const qlora_status st = p->bn == 64    ? SkinnyVariant<64, AMN, BMN, GROUPED>::prepare(maxc, &p->per_sm)
+                          : p->bn == 128 ? SkinnyVariant<128, AMN, BMN, GROUPED>::prepare(maxc, &p->per_sm)
+                                         : SkinnyVariant<256, AMN, BMN, GROUPED>::prepare(maxc, &p->per_sm);
   const int row_tiles = static_cast<int>(cdiv(rows, 128));
   p->splits = 1;
   for (int l = 3; l >= 1; --l)
@@ -526,9 +529,9 @@ qlora_status plan_skinny_v(int64_t rows, int64_t kdim, int r, SkinnyPlan *p) {
   return st;
 }
 
-template <int BN, bool AMN, bool BMN>
+template <int BN, bool AMN, bool BMN, bool GROUPED = false>
 qlora_status run_skinny_bn(const SkinnyArgs &a, int grid, cudaStream_t st) {
-  using C = typename SkinnyVariant<BN, AMN, BMN>::C;
+  using C = typename SkinnyVariant<BN, AMN, BMN, GROUPED>::C;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(C::THREADS);
@@ -548,11 +551,11 @@ qlora_status run_skinny_bn(const SkinnyArgs &a, int grid, cudaStream_t st) {
   return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
-template <bool AMN, bool BMN>
+template <bool AMN, bool BMN, bool GROUPED = false>
 qlora_status run_skinny(const SkinnyArgs &a, int bn, int grid, cudaStream_t st) {
-  if (bn == 64) return run_skinny_bn<64, AMN, BMN>(a, grid, st);
-  if (bn == 128) return run_skinny_bn<128, AMN, BMN>(a, grid, st);
-  return run_skinny_bn<256, AMN, BMN>(a, grid, st);
+  if (bn == 64) return run_skinny_bn<64, AMN, BMN, GROUPED>(a, grid, st);
+  if (bn == 128) return run_skinny_bn<128, AMN, BMN, GROUPED>(a, grid, st);
+  return run_skinny_bn<256, AMN, BMN, GROUPED>(a, grid, st);
 }
 
 
@@ -787,19 +790,20 @@ int skinny_ctas(int64_t rows, int64_t kdim, int r) {
   return static_cast<int>(cdiv(rows, 128)) * p.splits;
 }
 
-template <int NT, bool F16>
+template <int NT, bool F16, bool GROUPED = false>
 qlora_status run_smallm_nt(const SmallmArgs &a, int grid, cudaStream_t st) {
-  using C = SmallmCfg<NT>;
+  using C = SmallmCfg<NT, GROUPED>;
   static std::once_flag once[kMaxDevices];
   int dev = 0;
   cudaGetDevice(&dev);
   cudaError_t attr_err = cudaSuccess;
   std::call_once(once[dev], [&] {
     attr_err =
-        cudaFuncSetAttribute(smallm_kernel<NT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+        cudaFuncSetAttribute(smallm_kernel<NT, F16, GROUPED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::SMEM_BYTES);
   });
   if (attr_err != cudaSuccess) return QLORA_ERR_CUDA;
-  return launch_pdl(smallm_kernel<NT, F16>, grid, C::THREADS, C::SMEM_BYTES, st, a);
+  return launch_pdl(smallm_kernel<NT, F16, GROUPED>, grid, C::THREADS, C::SMEM_BYTES, st, a);
 }
 
 qlora_status run_smallm(const SmallmArgs &a, const SmallmPlan &p, cudaStream_t st) {
@@ -867,6 +871,8 @@ qlora_status check_linear(const uint8_t *packed, const uint8_t *q, const float *
   if (!aligned16(packed) || !aligned16(q) || !aligned16(scale2)) return QLORA_ERR_ALIGN;
   return check_tables(nf4, t8);
 }
+
+#include "grouped_host.cuh"
 
 }  // namespace
 
@@ -1676,6 +1682,114 @@ qlora_status qlora_paged_adamw_step(qlora_paged_adamw *opt, void *const *params,
   h.f16 = dtype == QLORA_F16 ? 1 : 0;
   if (!(h.bc1 > 0.0f) || !(h.bc2 > 0.0f)) return QLORA_ERR_RANGE;  // beta^t rounds to 1 only for beta = 1
   return adamw_launch(opt, params, grads, false, h, st);
+}
+
+// ------------------------------------------- expert groups and dropout --
+namespace {
+
+// Checks that the grouped forward and backward share, in the order of the
+// dense calls; NULL or misaligned pointers are the callers' (`ptrs`, required
+// unless there are no tokens).
+qlora_status check_grouped_call(const uint8_t *packed, const uint8_t *q, const float *scale2, const float *nf4,
+                                const float *t8, qlora_dtype dtype, const GroupedShape &s, const int32_t *offsets,
+                                float alpha, std::initializer_list<const void *> token_ptrs,
+                                std::initializer_list<const void *> ptrs, const void *XA, const void *workspace) {
+  if (dtype != QLORA_BF16 && dtype != QLORA_F16) return QLORA_ERR_RANGE;
+  if (!packed || !q || !scale2 || !nf4 || !t8) return QLORA_ERR_NULL;
+  const qlora_status st = check_grouped(s);
+  if (st != QLORA_OK) return st;
+  if (!std::isfinite(alpha)) return QLORA_ERR_RANGE;
+  if (!offsets && s.E != 1) return QLORA_ERR_NULL;
+  if (!aligned16(packed) || !aligned16(q) || !aligned16(scale2)) return QLORA_ERR_ALIGN;
+  for (const void *p : ptrs)
+    if (!p) return QLORA_ERR_NULL;
+  if (s.T > 0)
+    for (const void *p : token_ptrs)
+      if (!p) return QLORA_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(offsets) & 3u) return QLORA_ERR_ALIGN;
+  for (const void *p : ptrs)
+    if (!aligned16(p)) return QLORA_ERR_ALIGN;
+  for (const void *p : token_ptrs)
+    if (!aligned16(p)) return QLORA_ERR_ALIGN;
+  if (!aligned16(XA) || !aligned16(workspace)) return QLORA_ERR_ALIGN;
+  return check_tables(nf4, t8);
+}
+
+}  // namespace
+
+qlora_status qlora_dropout(const void *x, void *y, int64_t n, qlora_element type, const qlora_dropout_desc *drop,
+                           qlora_stream_t stream) {
+  if (type != QLORA_ELEMENT_BF16 && type != QLORA_ELEMENT_F16 && type != QLORA_ELEMENT_F32) return QLORA_ERR_RANGE;
+  if (!drop) return QLORA_ERR_NULL;
+  if (n < 0) return QLORA_ERR_SHAPE;
+  if (n > 0 && (!x || !y)) return QLORA_ERR_NULL;
+  if (!aligned16(x) || !aligned16(y)) return QLORA_ERR_ALIGN;
+  DropoutArgs d;
+  qlora_status st = make_dropout(drop, &d);
+  if (st != QLORA_OK) return st;
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != QLORA_OK) return st;
+  if (n == 0) return QLORA_OK;
+  return run_dropout(x, y, n, static_cast<int>(type), d, d.factor, dev.sms, static_cast<cudaStream_t>(stream));
+}
+
+size_t qlora_grouped_workspace_bytes(int E, int64_t T, int64_t N, int64_t K, int r, int dropout) {
+  const GroupedShape s{E, T, N, K, r, dropout != 0};
+  if (check_grouped(s) != QLORA_OK) return 0;
+  if (T == 0) return 256;
+  DeviceInfo d;
+  int sms = 148;
+  if (device_info(&d) == QLORA_OK) sms = d.sms;
+  const GroupedFwdPlan f = plan_grouped_fwd(s, sms);
+  const GroupedBwdPlan b = plan_grouped_bwd(s, sms);
+  return std::max(grouped_ws(s, f.counters, f.part, false).total, grouped_ws(s, b.counters, b.part, true).total);
+}
+
+qlora_status qlora_grouped_linear_fwd(const uint8_t *packed, const uint8_t *q, const float *scale2,
+                                      const float nf4[16], const float t8[256], qlora_dtype dtype, int E, int64_t T,
+                                      int64_t N, int64_t K, const int32_t *offsets, const void *X, const void *A,
+                                      const void *B, int r, float alpha, const qlora_dropout_desc *drop, void *Y,
+                                      void *XA_out, void *workspace, size_t workspace_bytes, qlora_stream_t stream) {
+  GroupedShape s{E, T, N, K, r, false};
+  qlora_status st = check_grouped_call(packed, q, scale2, nf4, t8, dtype, s, offsets, alpha, {X, Y}, {A, B}, XA_out,
+                                       workspace);
+  if (st != QLORA_OK) return st;
+  DropoutArgs d;
+  if ((st = make_dropout(drop, &d)) != QLORA_OK) return st;
+  s.drop = d.threshold != 0;
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != QLORA_OK) return st;
+  if (T == 0) return QLORA_OK;
+  DtypeScope scope(dtype == QLORA_F16);
+  return grouped_fwd(packed, q, scale2, nf4, t8, s, offsets, X, A, B, alpha, d, Y, XA_out, workspace, workspace_bytes,
+                     dev.sms, static_cast<cudaStream_t>(stream));
+}
+
+qlora_status qlora_grouped_linear_bwd(const uint8_t *packed, const uint8_t *q, const float *scale2,
+                                      const float nf4[16], const float t8[256], qlora_dtype dtype, int E, int64_t T,
+                                      int64_t N, int64_t K, const int32_t *offsets, const void *X, const void *dY,
+                                      const void *A, const void *B, const void *XA, int r, float alpha,
+                                      const qlora_dropout_desc *drop, void *dX, void *dA, void *dB, void *workspace,
+                                      size_t workspace_bytes, qlora_stream_t stream) {
+  GroupedShape s{E, T, N, K, r, false};
+  qlora_status st = check_grouped_call(packed, q, scale2, nf4, t8, dtype, s, offsets, alpha, {X, dY, dX},
+                                       {A, B, dA, dB}, XA, workspace);
+  if (st != QLORA_OK) return st;
+  DropoutArgs d;
+  if ((st = make_dropout(drop, &d)) != QLORA_OK) return st;
+  s.drop = d.threshold != 0;
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != QLORA_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (T == 0) {  // no tokens: every adapter gradient is zero
+    if (cudaMemsetAsync(dA, 0, static_cast<size_t>(E) * K * r * 2, cs) != cudaSuccess ||
+        cudaMemsetAsync(dB, 0, static_cast<size_t>(E) * r * N * 2, cs) != cudaSuccess)
+      return QLORA_ERR_CUDA;
+    return QLORA_OK;
+  }
+  DtypeScope scope(dtype == QLORA_F16);
+  return grouped_bwd(packed, q, scale2, nf4, t8, s, offsets, X, dY, A, B, XA, alpha, d, dX, dA, dB, workspace,
+                     workspace_bytes, dev.sms, cs);
 }
 
 }  // extern "C"

@@ -16,9 +16,21 @@
 //
 // Roles: warp 0 TMA, warp 1 TMEM + MMA issue, warps 4-7 TMEM readout (lane
 // quadrant = warp - 4); all 8 warps take part in the cluster reduction.
+//
+// Expert groups (GROUPED = true; groups.cuh). Products over token rows (X A,
+// dY B^T): a tile is 128 rows of one expert, clusters past the last tile
+// leave at once (the host sizes the grid for the worst split of the tokens).
+// Products over the tokens (X^T G, dY^T XA; A_MN): a tile is (expert, 128
+// output rows), reduced over that expert's tokens alone. Its first token
+// need not be a multiple of anything (it is a row coordinate), but the last
+// 64-token block may reach into the next expert's rows: warp 2 sets those
+// rows of both operands to zero in shared memory before the MMAs read them,
+// so that not even a NaN there can enter this expert's gradient. An expert
+// without tokens gets zeros.
 #pragma once
 
 #include "codec.cuh"
+#include "groups.cuh"
 #include "ptx.cuh"
 
 namespace qlora {
@@ -51,10 +63,12 @@ struct SkinnyArgs {
               // the kernel before it, so the whole product runs without waiting for that kernel; each
               // thread waits for it only before exiting, so this grid still completes after it
   int f16;   // operands and outputs are fp16 (else bf16)
+  GroupArgs groups;  // GROUPED only; prob[i].rows is then per expert for products over the tokens
 };
 
-template <int BN_, bool A_MN_, bool B_MN_, int STAGES_>
+template <int BN_, bool A_MN_, bool B_MN_, int STAGES_, bool GROUPED_ = false>
 struct SkinnyCfg {
+  static constexpr bool GROUPED = GROUPED_;
   static constexpr int BN = BN_, STAGES = STAGES_;
   static constexpr bool A_MN = A_MN_, B_MN = B_MN_;
   static_assert(BN_ % 64 == 0 && BN_ <= 256, "rank tile");
@@ -63,9 +77,10 @@ struct SkinnyCfg {
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = STAGES_ * A_BYTES;
   static constexpr int OFF_BAR = OFF_B + STAGES_ * B_BYTES;
-  static constexpr int NBARS = 2 * STAGES_ + 2;  // full[S], empty[S], tmem_full, drain
+  static constexpr int NBARS = 2 * STAGES_ + (GROUPED_ ? 4 : 2);  // full[S], empty[S], tmem_full, drain, (landed, tail)
   static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
-  static constexpr int SMEM_BYTES = OFF_MISC + 16;
+  static constexpr int OFF_GROUPS = OFF_MISC + 16;
+  static constexpr int SMEM_BYTES = OFF_GROUPS + (GROUPED_ ? kGroupTableBytes : 0);
   static constexpr int THREADS = 256;
   static constexpr uint32_t TMEM_COLS = BN_ <= 64 ? 64 : (BN_ <= 128 ? 128 : 256);
   static constexpr int PART_LD = BN_ + 4;  // fp32 per partial row (16-byte pad against bank conflicts)
@@ -95,10 +110,40 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
   const int local_block = static_cast<int>(blockIdx.x) - (pi ? args.prob0_ctas : 0);
   const uint32_t rank = splits > 1 ? cluster_ctarank() : 0u;
   const int tile = local_block / splits;
-  const int row0 = tile * 128;
-  const int kb_begin = static_cast<int>((static_cast<int64_t>(rank) * P.kblocks) / splits);
-  const int kb_end = static_cast<int>((static_cast<int64_t>(rank + 1) * P.kblocks) / splits);
+  const uint32_t landed_bar = bar0 + 8u * (2 * C::STAGES + 2), tail_bar = landed_bar + 8u;
+  int row0 = tile * 128;
+  int row_end = P.rows;    // one past the tile's last row
+  int kblocks = P.kblocks;
+  int group = 0;           // expert
+  int tok0 = 0, ntok = 0;  // products over the tokens: the expert's first token and count
+  if constexpr (C::GROUPED) {
+    // late launches run on inputs that are complete when they start
+    if (!args.late) grid_dep_wait();
+    const GroupTable gt = group_table(smem + C::OFF_GROUPS);
+    if (warp == 0) build_group_table(args.groups, 128, gt);
+    __syncthreads();
+    if constexpr (C::A_MN) {
+      const int row_tiles = (P.rows + 127) / 128;
+      group = tile / row_tiles;
+      row0 = (tile - group * row_tiles) * 128;
+      tok0 = gt.first[group];
+      ntok = gt.first[group + 1] - tok0;
+      kblocks = (ntok + 63) / 64;
+    } else {
+      if (tile >= gt.cum[args.groups.groups]) {  // the whole cluster leaves
+        grid_dep_launch();
+        return;
+      }
+      group = group_of_tile(gt, args.groups.groups, tile);
+      row0 = gt.first[group] + (tile - gt.cum[group]) * 128;
+      row_end = gt.first[group + 1];
+    }
+  }
+  const int kb_begin = static_cast<int>((static_cast<int64_t>(rank) * kblocks) / splits);
+  const int kb_end = static_cast<int>((static_cast<int64_t>(rank + 1) * kblocks) / splits);
   const int nk = kb_end - kb_begin;
+  // this CTA's last block ends inside: its rows past the expert's last token are zeroed
+  const int tail_rows = C::GROUPED && C::A_MN && nk > 0 && kb_end == kblocks ? ntok & 63 : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -107,6 +152,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
     }
     mbar_init(tmem_full, 1);
     mbar_init(drain_bar, 1);
+    if (C::GROUPED) {
+      mbar_init(landed_bar, 1);
+      mbar_init(tail_bar, 1);
+    }
     *s_abort = 0;
     fence_barrier_init();
   }
@@ -131,6 +180,25 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
     const uint32_t a_dst = sbase + C::OFF_A + s * C::A_BYTES;
     const uint32_t b_dst = sbase + C::OFF_B + s * C::B_BYTES;
     mbar_arrive_expect_tx(full_bar(s), C::TX);
+    if constexpr (C::GROUPED) {
+      if (C::A_MN) {  // token rows of both operands from the expert's first one on
+        const int tok = tok0 + kb * 64;
+        tma_load_2d(a_dst, &P.tm_a, full_bar(s), row0, tok);
+        tma_load_2d(a_dst + 8192, &P.tm_a, full_bar(s), row0 + 64, tok);
+#pragma unroll
+        for (int c = 0; c < C::BN / 64; ++c) tma_load_2d(b_dst + c * 8192, &P.tm_b, full_bar(s), c * 64, tok);
+      } else {  // the expert's adapter: a slice of a 3-D map
+        tma_load_2d(a_dst, &P.tm_a, full_bar(s), kb * 64, row0);
+        if (C::B_MN) {
+#pragma unroll
+          for (int c = 0; c < C::BN / 64; ++c)
+            tma_load_3d(b_dst + c * 8192, &P.tm_b, full_bar(s), c * 64, kb * 64, group);
+        } else {
+          tma_load_3d(b_dst, &P.tm_b, full_bar(s), kb * 64, 0, group);
+        }
+      }
+      return;
+    }
     if (C::A_MN) {
       tma_load_2d(a_dst, &P.tm_a, full_bar(s), row0, kb * 64);
       tma_load_2d(a_dst + 8192, &P.tm_a, full_bar(s), row0 + 64, kb * 64);
@@ -144,9 +212,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
       tma_load_2d(b_dst, &P.tm_b, full_bar(s), kb * 64, 0);
     }
   };
-  if (args.early && !args.late && warp == 0 && lane == 0)
+  if (!C::GROUPED && args.early && !args.late && warp == 0 && lane == 0)
     for (; issued < nk && issued < C::STAGES; ++issued) issue(issued);
-  if (!args.late) grid_dep_wait();
+  if (!C::GROUPED && !args.late) grid_dep_wait();
   grid_dep_launch();
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < args.nzero; i += blockDim.x) args.zero_words[i] = 0u;
@@ -170,12 +238,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (lane == 0 && (!C::GROUPED || nk > 0)) {
       const uint32_t idesc = idesc_dtype(make_idesc_bf16(128, C::BN, C::A_MN ? 1 : 0, C::B_MN ? 1 : 0), args.f16);
       bool ok = true;
       for (int j = 0; j < nk; ++j) {
         const int s = j % C::STAGES;
         if (!mbar_wait(full_bar(s), (j / C::STAGES) & 1u, s_abort)) { ok = false; break; }
+        if (C::GROUPED && tail_rows > 0 && j == nk - 1) {
+          mbar_arrive(landed_bar);  // (only this thread follows the ring's phases)
+          if (!mbar_wait(tail_bar, 0, s_abort)) { ok = false; break; }
+        }
         tc_fence_after();
         const uint32_t a_addr = sbase + C::OFF_A + s * C::A_BYTES;
         const uint32_t b_addr = sbase + C::OFF_B + s * C::B_BYTES;
@@ -197,10 +269,30 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
       }
     }
     __syncwarp();
+  } else if (C::GROUPED && warp == 2) {
+    if (tail_rows > 0) {
+      // once the last block has landed, zero its rows past the expert's last
+      // token (a row is 128 consecutive bytes of each 64 x 64 chunk, whatever
+      // the swizzle), then let the MMA thread read it
+      const int s = (nk - 1) % C::STAGES;
+      if (warp_wait_all(landed_bar, 0, s_abort)) {
+        const int first = tail_rows * 8, per = 512 - first;  // 16-byte pieces of a chunk
+        constexpr int NCH = 2 + C::BN / 64;
+        for (int i = lane; i < per * NCH; i += 32) {
+          const int c = i / per, o = first + i - c * per;
+          uint8_t *chunk = c < 2 ? smem + C::OFF_A + s * C::A_BYTES + c * 8192
+                                 : smem + C::OFF_B + s * C::B_BYTES + (c - 2) * 8192;
+          *reinterpret_cast<uint4 *>(chunk + o * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tail_bar);
+      }
+    }
   } else if (warp >= 4) {
     // TMEM -> this CTA's fp32 partial in shared memory (the ring is idle now)
     const int q = warp - 4;
-    const bool ok = warp_wait_all(tmem_full, 0, s_abort);
+    const bool ok = (!C::GROUPED || nk > 0) && warp_wait_all(tmem_full, 0, s_abort);
     tc_fence_after();
     float *part = reinterpret_cast<float *>(smem);
     const int lrow = q * 32 + lane;
@@ -261,11 +353,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
         v = *reinterpret_cast<const float4 *>(smem + off);
       }
       const int row = row0 + lrow;
-      if (row >= P.rows) continue;
+      if (row >= row_end) continue;
       const float vv[4] = {v.x, v.y, v.z, v.w};
       for (int o = 0; o < 2; ++o) {
         uint16_t *dst = reinterpret_cast<uint16_t *>(o ? P.out2 : P.out);
         if (dst == nullptr) continue;
+        if constexpr (C::GROUPED && C::A_MN) dst += static_cast<int64_t>(group) * P.rows * P.cols;  // this expert's
         const float sc = o ? P.out2_scale : P.out_scale;
         const int64_t ld = o ? P.out2_ld : P.out_ld;
 #pragma unroll

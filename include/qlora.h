@@ -255,9 +255,10 @@ QLORA_API qlora_status qlora_linear_bwd_dt(const uint8_t *packed, const uint8_t 
 
 /*
  * The device error word of the current device: bit 0 = a bounded pipeline
- * wait ran out (the kernel returned early; its outputs are undefined).
- * Synchronizes the device. clear != 0 resets the word. Returns 0xFFFFFFFF if
- * the word cannot be read.
+ * wait ran out (the kernel returned early; its outputs are undefined);
+ * bit 1 = expert offsets were not ascending within [0, T]
+ * (qlora_grouped_linear_fwd). Synchronizes the device. clear != 0 resets the
+ * word. Returns 0xFFFFFFFF if the word cannot be read.
  */
 QLORA_API uint32_t qlora_device_error(int clear);
 
@@ -431,6 +432,99 @@ QLORA_API int qlora_paged_adamw_location(const qlora_paged_adamw *opt);
 QLORA_API size_t qlora_paged_adamw_state_bytes(const qlora_paged_adamw *opt);
 QLORA_API qlora_status qlora_paged_adamw_state(const qlora_paged_adamw *opt, float **master, float **m,
                                                float **v);
+
+/*
+ * Dropout from a counter-based generator (no counterpart on the pages, whose
+ * method leaves the adapters' training recipe open; adapters are commonly
+ * trained with dropout on the adapter branch's input).
+ *
+ * Whether element i of a tensor is kept is a pure function of (seed, offset,
+ * i): Philox4x32 with 10 rounds (Salmon, Moraes, Dror, Shaw, "Parallel random
+ * numbers: as easy as 1, 2, 3", SC'11) of the 64-bit counter offset + i / 8
+ * under the 64-bit key `seed` gives four 32-bit words; element i takes 16-bit
+ * half i % 8 of them (low half of word 0 first) and is kept where the half is
+ * at least t = floor(p 2^16 + 1/2). Kept elements are multiplied by
+ * 2^16 / (2^16 - t), the inverse of the exact keep probability; the others
+ * become +0, whatever they held. No mask is stored: a backward pass applies
+ * the same (p, seed, offset) to the gradient. A tensor of n elements uses the
+ * counters offset .. offset + ceil(n / 8) - 1 (mod 2^64): the caller advances
+ * `offset` by that between tensors.
+ *
+ * Requires 0 <= p and t < 2^16 (else QLORA_ERR_RANGE).
+ */
+typedef struct {
+  double p;
+  uint64_t seed;
+  uint64_t offset;
+} qlora_dropout_desc;
+
+typedef enum { QLORA_ELEMENT_BF16 = 0, QLORA_ELEMENT_F16 = 1, QLORA_ELEMENT_F32 = 2 } qlora_element;
+
+/*
+ * y[i] = kept(i) ? round(x[i] * factor) : 0 for i < n (fp32 product, one
+ * rounding). x, y: device, 16-byte aligned; y == x is allowed, any other
+ * overlap is not. n >= 0; n == 0 launches nothing and takes NULL pointers.
+ * `drop`: host.
+ */
+QLORA_API qlora_status qlora_dropout(const void *x, void *y, int64_t n, qlora_element type,
+                                     const qlora_dropout_desc *drop, qlora_stream_t stream);
+
+/*
+ * The linear of a mixture of experts: E frozen NF4 weights with an adapter
+ * pair each, the token rows sorted by expert (no counterpart on the pages;
+ * the layer of each expert is qlora_linear_fwd / qlora_linear_bwd's).
+ *   packed, q, scale2: the codec of the experts' weights stacked as one
+ *     [E N, K] matrix (second-level groups straddle experts as they straddle
+ *     rows).
+ *   offsets: device int32 [E + 1], ascending within [0, T]: expert e's rows of
+ *     X, Y, dY, dX and XA are offsets[e] .. offsets[e + 1] - 1. The host never
+ *     reads them, so a router's output can stay on the device. Rows before
+ *     offsets[0] and from offsets[E] on belong to no expert and are left as
+ *     they were in every output. An expert may have no rows (its weight is
+ *     then not read, its dA and dB are zeros). NULL is allowed for E = 1: all
+ *     T rows, the dense linear. Offsets out of range or descending set bit 1
+ *     of the device error word; they are then clamped to [0, T] and raised to
+ *     the largest offset before them, so every access stays in bounds.
+ *   X, dY, Y, dX [T, K or N], XA [T, r]; A, dA [E, K, r]; B, dB [E, r, N];
+ *     16-bit in `dtype`.
+ *   drop: host, or NULL: adapter dropout D over X as a [T, K] tensor,
+ *       Y  = X W'^T + s (D(X) A) B,     XA = D(X) A
+ *       dX = dY W' + D'(G A^T),         G = s dY B^T
+ *       dA = D(X)^T G,                  dB = s XA^T dY
+ *     where D' multiplies by the same mask and factor; the backward gets the
+ *     same (p, seed, offset) as the forward. A dropped element's low-rank
+ *     term is exactly 0.
+ *   XA_out may be NULL (not saved); XA may be NULL (recomputed from X).
+ *   workspace: at least qlora_grouped_workspace_bytes(E, T, N, K, r, dropout)
+ *     bytes (enough for either direction; dropout: nonzero when `drop` drops
+ *     anything, p 2^16 >= 1/2). Calls that may overlap on the device need a
+ *     workspace each.
+ * Accumulation is fp32; s X A and G are rounded to 16 bits before their
+ * rank-r products, everything else once. Experts are isolated: a NaN or an
+ * infinity in one expert's rows or adapters reaches that expert's outputs
+ * only.
+ * Requires 1 <= E <= QLORA_MAX_EXPERTS, T >= 0 (T = 0: token pointers may be
+ * NULL; the backward zeroes dA and dB), N, K >= 64 and multiples of 64,
+ * E N and E K at most 2^30, 1 <= r <= 256, r % 8 == 0, alpha finite, 16-byte
+ * aligned pointers (offsets: 4). Outputs must not overlap inputs or each
+ * other. Both calls can be captured into a CUDA graph after one uncaptured
+ * call of the same kind.
+ */
+#define QLORA_MAX_EXPERTS 1024
+QLORA_API size_t qlora_grouped_workspace_bytes(int E, int64_t T, int64_t N, int64_t K, int r, int dropout);
+QLORA_API qlora_status qlora_grouped_linear_fwd(const uint8_t *packed, const uint8_t *q, const float *scale2,
+                                                const float nf4[16], const float t8[256], qlora_dtype dtype, int E,
+                                                int64_t T, int64_t N, int64_t K, const int32_t *offsets,
+                                                const void *X, const void *A, const void *B, int r, float alpha,
+                                                const qlora_dropout_desc *drop, void *Y, void *XA_out,
+                                                void *workspace, size_t workspace_bytes, qlora_stream_t stream);
+QLORA_API qlora_status qlora_grouped_linear_bwd(const uint8_t *packed, const uint8_t *q, const float *scale2,
+                                                const float nf4[16], const float t8[256], qlora_dtype dtype, int E,
+                                                int64_t T, int64_t N, int64_t K, const int32_t *offsets,
+                                                const void *X, const void *dY, const void *A, const void *B,
+                                                const void *XA, int r, float alpha, const qlora_dropout_desc *drop,
+                                                void *dX, void *dA, void *dB, void *workspace,
+                                                size_t workspace_bytes, qlora_stream_t stream);
 
 /*
  * Measurement instrumentation (no counterpart on the pages).
