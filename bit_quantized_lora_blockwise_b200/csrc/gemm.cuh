@@ -94,7 +94,7 @@ struct GemmArgs {
   // Output: 16-bit (bf16, or fp16 when f16) out[col * out_ld + row] (the transposed tile).
   void *out;
   int64_t out_ld;
-  float *part;             // fp32 partials of split tiles [tail_splits][tail tiles][tile columns][TILE_ROWS]
+  float *part;             // fp32 partials of split tiles [tail_splits][tail tiles][tile columns / 4][TILE_ROWS][4]
   unsigned int *counters;  // one per split output tile; zero on entry, left zero
   int rows;               // extent of the weight-row MMA dimension
   int cols;               // extent of the token MMA dimension
@@ -309,6 +309,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
     mbar_init(drain_bar, 1);
     mbar_init(epi_bar, 4);
     *s_abort = 0;
+    *reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8) = 0;  // s_last
     fence_barrier_init();
   }
   if (threadIdx.x < 16) reinterpret_cast<float *>(smem + C::OFF_MISC + 16)[threadIdx.x] = args.nf4[threadIdx.x];
@@ -430,9 +431,77 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
     }
   };
 
+  // first token of the 32 columns of chunk ch of sub-tile st (they never
+  // straddle the CTA halves)
+  auto chunk_token = [&](const TileCoord &t, int st, int ch) {
+    const int c0 = ch * 32;
+    if constexpr (C::GROUPED) {
+      const int hi = c0 >= t.half ? 1 : 0;
+      return t.col0 + hi * t.nst * t.half + st * t.half + c0 - hi * t.half;
+    } else {
+      return t.col0 + (c0 / C::B_ROWS) * C::CTA_TOK + st * C::B_ROWS + c0 % C::B_ROWS;
+    }
+  };
+  auto tile_end = [&](const TileCoord &t) { return C::GROUPED ? t.end : args.cols; };
+  auto tile_chunks = [&](const TileCoord &t) { return C::GROUPED ? t.half / 16 : C::NCHUNK; };  // with columns
+  auto tile_subs = [&](const TileCoord &t) { return C::GROUPED ? t.nst : C::NTT; };
+  // fp32 partials of the split tiles, rows padded to whole 32-column chunks
+  // per sub-tile. Partial of split sp of tail tile ti: first float4 of this
+  // CTA's row qrow, chunk 0. Four columns of a row are adjacent and rows
+  // follow one another, so a chunk is 8 accesses of 512 contiguous bytes per
+  // warp, the next chunk 8 TILE_ROWS float4 further.
+  constexpr int TILE_PCOLS = C::NTT * C::NCHUNK * 32;
+  const int ntail = C::GROUPED ? gp.tiles - gp.full_tiles : row_tiles * col_tiles - args.full_tiles;
+  auto part_at = [&](int sp, int ti, int qrow) {
+    return reinterpret_cast<float4 *>(args.part) +
+           (static_cast<int64_t>(sp) * ntail + ti) * (TILE_PCOLS / 4) * C::TILE_ROWS + rank * 128 + qrow;
+  };
+  volatile int *s_last = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8);
+  // out[token][row] for the 32 consecutive tokens from tok (clipped at
+  // `end`) and the warp's 32 rows (all in range or none: rows is a multiple
+  // of 64). A thread holds one row of 32 tokens; three exchanges between
+  // lanes that differ in bit 0, 1 and 2 give it 8 consecutive rows of the
+  // four tokens 8 n + (lane & 7), so that a store moves 16 bytes a lane and
+  // 64 per token. (One 2-byte store per element took 20 us of a 101 us call
+  // on 18944 x 4096 with 512 tokens; this one 4.)
+  auto store_out = [&](int row, int tok, int end, const float (&v)[32]) {
+    if (row - lane >= args.rows) return;
+    const bool f16 = args.f16 != 0;
+    const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t own = pack_16x2(v[2 * i], v[2 * i + 1], f16);
+      w[i] = prmt(own, __shfl_xor_sync(0xFFFFFFFFu, own, 1), sel);  // token 2 i + bit 0, two rows
+    }
+    const bool b1 = lane & 2, b2 = lane & 4;
+    uint32_t x[8][2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // token 4 i + 2 bit 1 + bit 0, four rows
+      const uint32_t own = b1 ? w[2 * i + 1] : w[2 * i];
+      const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, b1 ? w[2 * i] : w[2 * i + 1], 2);
+      x[i][0] = b1 ? got : own;
+      x[i][1] = b1 ? own : got;
+    }
+    uint16_t *dst = reinterpret_cast<uint16_t *>(args.out) + (row - lane) + (lane >> 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t own[2], got[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        own[h] = b2 ? x[2 * i + 1][h] : x[2 * i][h];
+        got[h] = __shfl_xor_sync(0xFFFFFFFFu, b2 ? x[2 * i][h] : x[2 * i + 1][h], 4);
+      }
+      const int token = tok + 8 * i + (lane & 7);
+      if (token < end)
+        *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(token) * args.out_ld) =
+            b2 ? make_uint4(got[0], got[1], own[0], own[1]) : make_uint4(own[0], own[1], got[0], got[1]);
+    }
+  };
+
   if (warp == 4) {
     // --------------------------------- TMA: token stages, low-rank operands --
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t job = 0, bs = 0;  // A-ring job and B-ring stage counters
       bool ok = true;
       bool waited = false;
@@ -516,7 +585,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
     // CTAs' stages (same offsets), so the leader's barriers count both CTAs'
     // copies and producers, and its commits release the stage in both CTAs
     // (mask 0b11).
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       constexpr uint64_t DK = smem_desc_const(16, 1024);    // K-major, 128B swizzle
       constexpr uint64_t DM = smem_desc_const(8192, 1024);  // MN-major, 128B swizzle
       constexpr int IDN = C::GROUPED ? 0 : C::BN;  // grouped: the columns of each tile
@@ -607,24 +676,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
     __syncwarp();
   } else if (warp < 4) {
     // ------------------------------------------------------- epilogue --
-    auto qrow_of = [](int w, int l) { return w * 32 + l; };
-    // A whole tile: TMEM -> bf16 output directly. A split tile: TMEM -> fp32
-    // partial in global memory; the last of the tile's splits to arrive
-    // (atomic counter) sums the partials in split order (deterministic) and
-    // writes the bf16 output.
-    volatile int *s_last = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8);
-    // partial rows are padded to whole 32-column chunks per sub-tile
-    constexpr int TILE_PCOLS = C::NTT * C::NCHUNK * 32;
-    const int ntail = C::GROUPED ? gp.tiles - gp.full_tiles : row_tiles * col_tiles - args.full_tiles;
-    // Partial of split sp of tail tile ti, column-major ([column][row]) so
-    // that the 32 threads of a warp (32 consecutive rows) store and load 128
-    // contiguous bytes: this thread's element of column c is part_col(..)[c * TILE_ROWS].
-    auto part_col = [&](int sp, int ti) {
-      return args.part + (static_cast<int64_t>(sp) * ntail + ti) * TILE_PCOLS * C::TILE_ROWS + rank * 128 +
-             qrow_of(warp, lane);
-    };
+    // A whole tile: TMEM -> 16-bit output directly. A split tile: TMEM -> fp32
+    // partial in global memory; the CTA that brings the tile's count to its
+    // number of splits sums them at the end of the kernel.
     uint32_t iter = 0, epi_phase = 0;
-    const int qrow = qrow_of(warp, lane);  // TMEM lane of this thread
+    const int qrow = warp * 32 + lane;  // TMEM lane of this thread
     // chunk ch of the accumulator row (32 columns; a 16-column tail is zero-padded)
     auto load_chunk = [&](uint32_t tcol, int ch, uint32_t (&u)[32]) {
       if (C::BN % 32 == 16 && ch == C::NCHUNK - 1) {
@@ -639,17 +695,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
         tmem_ld_32x32b_x32(tcol + ch * 32, u);
       }
     };
-    // out[token][row] for the 32 consecutive tokens from tok (clipped at
-    // `end`); each warp store covers 32 consecutive rows
-    auto store_out = [&](int row, int tok, int end, const float (&v)[32]) {
-      if (row >= args.rows) return;
-      const int ncol = end - tok < 32 ? end - tok : 32;
-      uint16_t *dst = reinterpret_cast<uint16_t *>(args.out);
-      const bool f16 = args.f16 != 0;
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < ncol) dst[static_cast<int64_t>(tok + j) * args.out_ld + row] = to_16(v[j], f16);
-    };
     bool ok = true;
     for (int tile = first_tile; ok && tile < num_tiles; tile += tile_step, ++iter) {
       const TileCoord t = coord(tile);
@@ -658,19 +703,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
         continue;
       }
       const int row = t.row0 + qrow;
-      const int end = C::GROUPED ? t.end : args.cols;
-      const int nchunk = C::GROUPED ? t.half / 16 : C::NCHUNK;  // chunks with columns, per sub-tile
-      const int nsub = C::GROUPED ? t.nst : C::NTT;
-      // first token of chunk ch of sub-tile st (32 columns never straddle the CTA halves)
-      auto tok0 = [&](int st, int ch) {
-        const int c0 = ch * 32;
-        if constexpr (C::GROUPED) {
-          const int hi = c0 >= t.half ? 1 : 0;
-          return t.col0 + hi * t.nst * t.half + st * t.half + c0 - hi * t.half;
-        } else {
-          return t.col0 + (c0 / C::B_ROWS) * C::CTA_TOK + st * C::B_ROWS + c0 % C::B_ROWS;
-        }
-      };
+      const int end = tile_end(t), nchunk = tile_chunks(t), nsub = tile_subs(t);
+      auto tok0 = [&](int st, int ch) { return chunk_token(t, st, ch); };
       // SEP: keep bits of the 32 rows of this warp for token tok0(0, ch) +
       // lane, evaluated while the tile's MMAs run
       uint32_t keep[C::SEP ? C::NCHUNK : 1];
@@ -688,7 +722,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
           keep[ch] = word;
         }
       }
-      float *pcol = t.nsplit > 1 ? part_col(t.split, t.tail) : nullptr;
+      float4 *pcol = t.nsplit > 1 ? part_at(t.split, t.tail, qrow) : nullptr;
 #pragma unroll 1
       for (int st = 0; st < C::NTT; ++st) {
         const uint32_t u = iter * C::USES + st;
@@ -703,6 +737,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
         const uint32_t tcol = tmem_base + ((uint32_t)(warp * 32) << 16) + (u & 1u) * C::ACC_STRIDE;
 #pragma unroll 1
         for (int ch = 0; ch < nchunk; ++ch) {
+          if (tok0(st, ch) >= end) continue;  // no token in these columns
           uint32_t w[32];
           load_chunk(tcol, ch, w);
           if constexpr (C::SEP) {
@@ -724,9 +759,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
             for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]);
             store_out(row, tok0(st, ch), end, v);
           } else {
-            float *o = pcol + static_cast<int64_t>((st * C::NCHUNK + ch) * 32) * C::TILE_ROWS;
+            float4 *o = pcol + (st * C::NCHUNK + ch) * 8 * C::TILE_ROWS;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) __stcg(o + j * C::TILE_ROWS, __uint_as_float(w[j]));
+            for (int j = 0; j < 8; ++j)
+              __stcg(o + j * C::TILE_ROWS,
+                     make_float4(__uint_as_float(w[4 * j]), __uint_as_float(w[4 * j + 1]),
+                                 __uint_as_float(w[4 * j + 2]), __uint_as_float(w[4 * j + 3])));
           }
         }
         tc_fence_before();
@@ -742,30 +780,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
         const int last = prev == static_cast<unsigned int>(t.nsplit - 1);
         if (last) args.counters[t.rc] = 0u;  // every split has arrived: reset for the next use
         *s_last = last;
-      }
-      if (!warp_group_sync(epi_bar, epi_phase, s_abort)) { ok = false; continue; }
-      if (*s_last) {
         __threadfence();
-#pragma unroll 1
-        for (int pc = 0; pc < C::NTT * C::NCHUNK; ++pc) {
-          if (C::GROUPED && (pc / C::NCHUNK >= nsub || pc % C::NCHUNK >= nchunk)) continue;  // no columns there
-          float v[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-          for (int sp = 0; sp < t.nsplit; ++sp) {
-            const float *src = part_col(sp, t.tail) + static_cast<int64_t>(pc * 32) * C::TILE_ROWS;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] += __ldcg(src + j * C::TILE_ROWS);
-          }
-          store_out(row, tok0(pc / C::NCHUNK, pc % C::NCHUNK), end, v);
-        }
       }
     }
   } else if (warp == 6) {
     // ------------------------------------------------ P ring: TMA issue --
     // Runs up to SP superjobs ahead of the producers, gated only by them:
     // the packed codes of the 128 x (64 KSUP) weight tile.
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t ms = 0;  // superjob counter (KSUP main jobs each, per tile)
       bool ok = true;
       for (int tile = first_tile; ok && tile < num_tiles; tile += tile_step) {
@@ -923,6 +945,34 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
     tc_fence_after();
     if constexpr (C::PAIR) tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
     else tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+  // The last split of a tile sums the partials, in split order
+  // (deterministic), with every warp of the CTA: a launch with split tiles has
+  // at most one unit per CTA, so the other roles are done. (Summed by the
+  // four epilogue warps the same 4 x 256 x 256 partials took 26 us.)
+  if (*s_last) {
+    const TileCoord t = coord(first_tile);
+    const int end = tile_end(t), nchunk = tile_chunks(t), nsub = tile_subs(t);
+    for (int i = warp; i < 4 * C::NTT * C::NCHUNK; i += C::WARPS) {
+      const int quad = i & 3, pc = i >> 2, st = pc / C::NCHUNK, ch = pc % C::NCHUNK;
+      const int tok = chunk_token(t, st, ch);
+      if (st >= nsub || ch >= nchunk || tok >= end) continue;  // no columns there
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+      for (int sp = 0; sp < t.nsplit; ++sp) {
+        const float4 *src = part_at(sp, t.tail, quad * 32 + lane) + pc * 8 * C::TILE_ROWS;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float4 p = __ldcg(src + j * C::TILE_ROWS);
+          v[4 * j] += p.x;
+          v[4 * j + 1] += p.y;
+          v[4 * j + 2] += p.z;
+          v[4 * j + 3] += p.w;
+        }
+      }
+      store_out(t.row0 + quad * 32 + lane, tok, end, v);
+    }
   }
 }
 

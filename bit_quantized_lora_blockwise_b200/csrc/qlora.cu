@@ -658,7 +658,7 @@ qlora_status skinny(SkinnyKind kind, const void *aop, int64_t a_inner, int64_t a
 // cluster of two CTAs): six token stages of one K block of 128 tokens (one
 // 16 KB TMA box each), dequantized-weight stages of one K block (16 KB) and
 // packed-code slots of 4 K blocks (18 KB).
-constexpr int kPairBkb = 1, kPairSb = 6, kPairSa = 4, kPairSp = 2, kPairNpw = 8;
+constexpr int kPairBkb = 1, kPairSb = 4, kPairSa = 5, kPairSp = 3, kPairNpw = 16;
 using FwdPairCfg = GemmCfg<256, A_DEQ_K, L2_A_MN, kPairBkb, kPairSb, kPairSa, kPairSp, kPairNpw, true>;
 using BwdPairCfg = GemmCfg<256, A_DEQ_MN, L2_A_K, kPairBkb, kPairSb, kPairSa, kPairSp, kPairNpw, true>;
 // Two 256-token sub-tiles per job (512 tokens per tile, each CTA loading 256
@@ -666,7 +666,7 @@ using BwdPairCfg = GemmCfg<256, A_DEQ_MN, L2_A_K, kPairBkb, kPairSb, kPairSa, kP
 // two of two blocks hide a refill behind three stages of MMAs, 2-3 % faster
 // on the 7B shapes), 3 dequantized-weight stages, 2 packed-code slots (212 KB
 // of shared memory).
-constexpr int kPair2Bkb = 1, kPair2Sb = 4, kPair2Sa = 3, kPair2Sp = 2, kPair2Npw = 8;
+constexpr int kPair2Bkb = 1, kPair2Sb = 3, kPair2Sa = 5, kPair2Sp = 2, kPair2Npw = 12;
 using FwdPair2Cfg = GemmCfg<256, A_DEQ_K, L2_A_MN, kPair2Bkb, kPair2Sb, kPair2Sa, kPair2Sp, kPair2Npw, true, 2>;
 using BwdPair2Cfg = GemmCfg<256, A_DEQ_MN, L2_A_K, kPair2Bkb, kPair2Sb, kPair2Sa, kPair2Sp, kPair2Npw, true, 2>;
 // token counts from which a tile holds two 256-token sub-tiles

@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && (!C::GROUPED || nk > 0)) {
+    if ((!C::GROUPED || nk > 0) && elect_one()) {
       const uint32_t idesc = idesc_dtype(make_idesc_bf16(128, C::BN, C::A_MN ? 1 : 0, C::B_MN ? 1 : 0), args.f16);
       bool ok = true;
       for (int j = 0; j < nk; ++j) {
