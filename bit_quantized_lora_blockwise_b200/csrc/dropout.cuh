@@ -43,6 +43,12 @@ __device__ __forceinline__ uint4 philox4x32_10(uint64_t seed, uint64_t counter) 
   return make_uint4(c0, c1, c2, c3);
 }
 
+// Whether the elements of a word's low and high half are kept: both 16-bit
+// compares in one packed maximum, whose predicates are half >= threshold.
+__device__ __forceinline__ void keep_pair(uint32_t word, uint32_t threshold, bool &lo, bool &hi) {
+  __vibmax_u16x2(word, threshold * 0x10001u, &hi, &lo);
+}
+
 // Keep bits of the eight elements of one counter (bit j: element j).
 __device__ __forceinline__ uint32_t dropout_keep8(const DropoutArgs &d, uint64_t group) {
   const uint4 w = philox4x32_10(d.seed, d.offset + group);
@@ -50,18 +56,23 @@ __device__ __forceinline__ uint32_t dropout_keep8(const DropoutArgs &d, uint64_t
   uint32_t keep = 0u;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    keep |= (u[j] & 0xFFFFu) >= d.threshold ? 1u << (2 * j) : 0u;
-    keep |= (u[j] >> 16) >= d.threshold ? 2u << (2 * j) : 0u;
+    bool lo, hi;
+    keep_pair(u[j], d.threshold, lo, hi);
+    keep |= (lo ? 1u << (2 * j) : 0u) | (hi ? 2u << (2 * j) : 0u);
   }
   return keep;
 }
 
 enum DropoutType : int { DROP_BF16 = 0, DROP_F16 = 1, DROP_F32 = 2 };
 
-// Eight elements: kept ones times the factor (fp32 product, one rounding),
-// the others +0, whatever they held (a dropped NaN or infinity is 0).
-template <int TYPE>
-__device__ __forceinline__ uint32_t dropout_pair(uint32_t v, uint32_t keep2, float factor) {
+// Two elements of a word's halves: kept ones times the factor (fp32 product,
+// one rounding), the others +0, whatever they held (a dropped NaN or infinity
+// is 0). SCALE = false: the factor is 1.
+template <int TYPE, bool SCALE>
+__device__ __forceinline__ uint32_t dropout_pair(uint32_t v, bool klo, bool khi, float factor) {
+  v = klo ? v : v & 0xFFFF0000u;
+  v = khi ? v : v & 0x0000FFFFu;
+  if constexpr (!SCALE) return v;
   float lo, hi;
   if constexpr (TYPE == DROP_F16) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v));
@@ -71,15 +82,28 @@ __device__ __forceinline__ uint32_t dropout_pair(uint32_t v, uint32_t keep2, flo
     lo = __uint_as_float(v << 16);
     hi = __uint_as_float(v & 0xFFFF0000u);
   }
-  lo = keep2 & 1u ? lo * factor : 0.0f;
-  hi = keep2 & 2u ? hi * factor : 0.0f;
-  return pack_16x2(lo, hi, TYPE == DROP_F16);
+  return pack_16x2(lo * factor, hi * factor, TYPE == DROP_F16);
+}
+
+// The same for the eight elements of one counter.
+template <int TYPE, bool SCALE>
+__device__ __forceinline__ uint4 dropout_eight(const uint4 &v, const DropoutArgs &d, uint64_t group, float factor) {
+  const uint4 w = philox4x32_10(d.seed, d.offset + group);
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w}, x[4] = {v.x, v.y, v.z, v.w};
+  uint32_t y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    bool lo, hi;
+    keep_pair(u[j], d.threshold, lo, hi);
+    y[j] = dropout_pair<TYPE, SCALE>(x[j], lo, hi, factor);
+  }
+  return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
 // y[i] = keep(i) ? x[i] * factor : 0 over n elements; x and y 16-byte
 // aligned, y == x allowed. One thread per counter (8 elements: one 16-byte
 // load and store for 16-bit types, two for fp32).
-template <int TYPE>
+template <int TYPE, bool SCALE = true>
 __global__ void __launch_bounds__(256) dropout_kernel(const void *x, void *y, int64_t n, const DropoutArgs d,
                                                       float factor) {
   grid_dep_wait();
@@ -99,10 +123,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const void *x, void *y, in
                       k & 128u ? b.w * factor : 0.0f);
     } else {
       const uint4 v = reinterpret_cast<const uint4 *>(x)[g];
-      const uint32_t k = dropout_keep8(d, static_cast<uint64_t>(g));
-      reinterpret_cast<uint4 *>(y)[g] =
-          make_uint4(dropout_pair<TYPE>(v.x, k, factor), dropout_pair<TYPE>(v.y, k >> 2, factor),
-                     dropout_pair<TYPE>(v.z, k >> 4, factor), dropout_pair<TYPE>(v.w, k >> 6, factor));
+      reinterpret_cast<uint4 *>(y)[g] = dropout_eight<TYPE, SCALE>(v, d, static_cast<uint64_t>(g), factor);
     }
   }
   // the last, partial counter: one thread, element by element
@@ -116,7 +137,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const void *x, void *y, in
         reinterpret_cast<float *>(y)[i] = (k >> j) & 1u ? v * factor : 0.0f;
       } else {
         const uint32_t v = reinterpret_cast<const uint16_t *>(x)[i];
-        reinterpret_cast<uint16_t *>(y)[i] = static_cast<uint16_t>(dropout_pair<TYPE>(v, (k >> j) & 1u, factor));
+        reinterpret_cast<uint16_t *>(y)[i] = static_cast<uint16_t>(dropout_pair<TYPE, SCALE>(v, (k >> j) & 1u, true, factor));
       }
     }
   }

@@ -68,12 +68,15 @@
 // split (whole tiles, by token sub-tile, or over K) is decided here from
 // the unit count, by the rule that the host uses for the dense call.
 //
-// Adapter dropout in dX (SEP = true): dX = dY W' + D(s G A^T), the mask
-// acting on the low-rank sum alone, so that sum has the second accumulator
-// to itself and the epilogue joins the two. A warp's 32 rows are four
-// counters of 8 consecutive k, so lane j evaluates the four counters of token
-// j: 32 keep bits, one per row, broadcast when column j is joined. They are
-// evaluated while the tile's MMAs run.
+// Adapter dropout in dX (DROP = true): dX = dY W' + D'(G A^T), the mask acting
+// on the low-rank sum alone. That sum is therefore formed first: the
+// low-rank K blocks run before the main ones, the epilogue warps take the
+// accumulator out of TMEM, zero what is dropped and put it back, and the main
+// K blocks accumulate on top. No second accumulator, no pass over dX, no
+// rounding of the term. A warp's 32 rows are four Philox counters of 8
+// consecutive k, so lane j evaluates the four counters of token j (32 keep
+// bits, one per row), and a bit transpose gives each row its word. The words
+// of a tile are evaluated while the tile before it runs.
 #pragma once
 
 #include "codec.cuh"
@@ -119,11 +122,11 @@ struct GemmArgs {
   // expert-grouped calls only
   GroupArgs groups;
   int expert_rows;    // N: weight rows of one expert
-  DropoutArgs drop;   // SEP: the adapter dropout of dX, over [tokens, rows]
+  DropoutArgs drop;   // DROP: the adapter dropout of dX, over [tokens, rows] (its factor is in B2)
 };
 
 template <int BN_, int ASRC_, int L2_, int BKB_, int SB_, int SA_, int SP_, int NPW_, bool PAIR_, int NTT_ = 1,
-          bool GROUPED_ = false, bool SEP_ = false>
+          bool GROUPED_ = false, bool DROP_ = false>
 struct GemmCfg {
   static constexpr int BM = 128, BK = 64, BN = BN_;
   static constexpr int ASRC = ASRC_, L2 = L2_;
@@ -131,11 +134,9 @@ struct GemmCfg {
   static constexpr bool PAIR = PAIR_;
   static constexpr int NTT = NTT_;                 // token sub-tiles (accumulators) per job
   static constexpr bool GROUPED = GROUPED_;        // tiles of expert groups
-  static constexpr bool SEP = SEP_;                // low-rank sum in accumulator 1, joined under the dropout mask
+  static constexpr bool DROP = DROP_;              // low-rank blocks first, their sum masked in TMEM
   static_assert(!GROUPED_ || (PAIR_ && BN_ == 256 && BKB_ == 1), "grouped tiles run on pairs, one K block per stage");
-  static_assert(!SEP_ || (GROUPED_ && NTT_ == 1), "a separate low-rank sum takes the second accumulator");
-  // accumulator uses per tile, as the phases count them
-  static constexpr int USES = SEP_ ? 2 : NTT_;
+  static_assert(!DROP_ || GROUPED_, "dropout comes with groups");
   static constexpr int NCTA = PAIR_ ? 2 : 1;       // CTAs per tile
   static constexpr int TILE_ROWS = 128 * NCTA;     // weight rows per tile
   static constexpr int TILE_COLS = BN_ * NTT_;     // tokens per tile
@@ -167,8 +168,8 @@ struct GemmCfg {
   static constexpr int OFF_P = OFF_A + SA * A_BYTES;
   static constexpr int OFF_BAR = OFF_P + SP * P_BYTES;
   // b_full[SB] b_empty[SB] a_full[SA] a_empty[SA] p_full[SP] p_empty[SP]
-  // tmem_full[2] tmem_empty[2] drain epilogue-group
-  static constexpr int NBARS = 2 * SB + 2 * SA + 2 * SP + 6;
+  // tmem_full[2] tmem_empty[2] drain epilogue-group (DROP: lora_full[2] masked[2])
+  static constexpr int NBARS = 2 * SB + 2 * SA + 2 * SP + 6 + (DROP_ ? 4 : 0);
   // misc: tmem base, abort flag, last-CTA flag (16 B), the 16 NF4 levels,
   // then the 256-entry 8-bit constant table
   static constexpr int OFF_MISC = ((OFF_BAR + NBARS * 8) + 15) & ~15;
@@ -286,6 +287,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
   auto tmem_empty = [&](int a) { return bar0 + 8u * (TB + 2 + a); };
   const uint32_t drain_bar = bar0 + 8u * (TB + 4);
   const uint32_t epi_bar = bar0 + 8u * (TB + 5);  // the four epilogue warps' group barrier
+  auto lora_full = [&](int a) { return bar0 + 8u * (TB + 6 + a); };  // DROP: low-rank sum complete
+  auto masked = [&](int a) { return bar0 + 8u * (TB + 8 + a); };     // DROP: and masked
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
   volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
 
@@ -305,6 +308,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
     for (int a = 0; a < 2; ++a) {
       mbar_init(tmem_full(a), 1);
       mbar_init(tmem_empty(a), C::GROUP_ARRIVALS);
+      if (C::DROP) {
+        mbar_init(lora_full(a), 1);
+        mbar_init(masked(a), C::GROUP_ARRIVALS);
+      }
     }
     mbar_init(drain_bar, 1);
     mbar_init(epi_bar, 4);
@@ -457,45 +464,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
            (static_cast<int64_t>(sp) * ntail + ti) * (TILE_PCOLS / 4) * C::TILE_ROWS + rank * 128 + qrow;
   };
   volatile int *s_last = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 8);
-  // out[token][row] for the 32 consecutive tokens from tok (clipped at
-  // `end`) and the warp's 32 rows (all in range or none: rows is a multiple
-  // of 64). A thread holds one row of 32 tokens; three exchanges between
-  // lanes that differ in bit 0, 1 and 2 give it 8 consecutive rows of the
-  // four tokens 8 n + (lane & 7), so that a store moves 16 bytes a lane and
-  // 64 per token. (One 2-byte store per element took 20 us of a 101 us call
-  // on 18944 x 4096 with 512 tokens; this one 4.)
+  // out[token][row] for the 32 consecutive tokens from tok (clipped at `end`)
+  // and the warp's 32 rows (all in range or none: rows is a multiple of 64),
+  // a thread holding one row: exchanged so that a lane stores 8 rows of a
+  // token, 16 bytes. (One 2-byte store per element took 20 us of a 101 us
+  // call on 18944 x 4096 with 512 tokens.)
   auto store_out = [&](int row, int tok, int end, const float (&v)[32]) {
     if (row - lane >= args.rows) return;
     const bool f16 = args.f16 != 0;
-    const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t own = pack_16x2(v[2 * i], v[2 * i + 1], f16);
-      w[i] = prmt(own, __shfl_xor_sync(0xFFFFFFFFu, own, 1), sel);  // token 2 i + bit 0, two rows
-    }
-    const bool b1 = lane & 2, b2 = lane & 4;
-    uint32_t x[8][2];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {  // token 4 i + 2 bit 1 + bit 0, four rows
-      const uint32_t own = b1 ? w[2 * i + 1] : w[2 * i];
-      const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, b1 ? w[2 * i] : w[2 * i + 1], 2);
-      x[i][0] = b1 ? got : own;
-      x[i][1] = b1 ? own : got;
-    }
     uint16_t *dst = reinterpret_cast<uint16_t *>(args.out) + (row - lane) + (lane >> 3) * 8;
+    uint4 q[4];
+    rows_to_columns(v, lane, f16, q);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint32_t own[2], got[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        own[h] = b2 ? x[2 * i + 1][h] : x[2 * i][h];
-        got[h] = __shfl_xor_sync(0xFFFFFFFFu, b2 ? x[2 * i][h] : x[2 * i + 1][h], 4);
-      }
       const int token = tok + 8 * i + (lane & 7);
-      if (token < end)
-        *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(token) * args.out_ld) =
-            b2 ? make_uint4(got[0], got[1], own[0], own[1]) : make_uint4(own[0], own[1], got[0], got[1]);
+      if (token < end) *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(token) * args.out_ld) = q[i];
     }
   };
 
@@ -522,7 +505,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
         // first token that this CTA loads: its half of every sub-tile, consecutive
         const int tok = t.col0 + static_cast<int>(rank) * (C::GROUPED ? t.nst * t.half : C::CTA_TOK);
         const int nbm = (t.nmain + C::BKB - 1) / C::BKB;
-        for (int st = 0; st < nbm + t.nlora; ++st, ++bs) {
+        for (int i = 0; i < nbm + t.nlora; ++i, ++bs) {
+          // stage st: the main ones, then the low-rank ones (DROP: low-rank first)
+          const int st = C::DROP ? (i < t.nlora ? nbm + i : i - t.nlora) : i;
           const int sb = bs % C::SB;
           if (!mbar_wait(b_empty(sb), ((bs / C::SB) & 1u) ^ 1u, s_abort)) { ok = false; break; }
           const uint32_t b_dst = sbase + C::OFF_B + sb * C::B_BYTES;
@@ -603,7 +588,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
         else tc_commit(bar);
       };
       const uint32_t a_base = sbase + C::OFF_A, b_base = sbase + C::OFF_B;
-      uint32_t job = 0, bs = 0, iter = 0;
+      uint32_t job = 0, bs = 0, iter = 0, mph = 0;  // mph: phases of masked(0), masked(1)
       bool ok = true;
       for (int tile = first_tile; ok && tile < num_tiles; tile += tile_step, ++iter) {
         const TileCoord t = coord(tile);
@@ -612,14 +597,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
           --iter;
           continue;
         }
-        // accumulator use u = iter * USES + sub-tile: accumulator u & 1, phase u >> 1
-        const uint32_t u0 = iter * C::USES;
+        // accumulator use u = iter * NTT + sub-tile: accumulator u & 1, phase u >> 1
+        const uint32_t u0 = iter * C::NTT;
         const int half = C::GROUPED ? t.half : C::B_ROWS;
         const uint32_t ncols = C::GROUPED ? static_cast<uint32_t>(2 * t.half) >> 3 << 17 : 0u;  // MMA N field
         int sa = job % C::SA;
         uint32_t pa = (job / C::SA) & 1u;
         for (int jj = 0; jj < njobs; ++jj, ++job) {
-          const bool main_job = jj < t.nmain;
+          const bool main_job = C::DROP ? jj >= t.nlora : jj < t.nmain;
           const int sub = main_job ? jj % C::BKB : 0;  // K block within the token stage
           const bool last_of_stage = !main_job || sub == C::BKB - 1 || jj == t.nmain - 1;
           const int sb = bs % C::SB;
@@ -644,13 +629,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
               if (jj == njobs - 1) commit(tmem_full(u & 1u));
               continue;
             }
-            const bool sep = C::SEP && !main_job;  // the low-rank sum's own accumulator
-            const uint32_t d_tmem = tmem_base + (sep ? 1u : u & 1u) * C::ACC_STRIDE;
+            if (C::DROP && t.nlora > 0 && jj == t.nlora) {  // the low-rank sum has been masked
+              if (!wait_full(masked(u & 1u), (mph >> (u & 1u)) & 1u)) { ok = false; break; }
+              mph ^= 1u << (u & 1u);
+              tc_fence_after();
+            }
+            const uint32_t d_tmem = tmem_base + (u & 1u) * C::ACC_STRIDE;
             const uint64_t bst = bd + ((st * half * 128) >> 4);  // sub-tile st's tokens of the stage
-            mma(d_tmem, ad, bst, idesc, jj > (sep ? t.nmain : 0) ? 1u : 0u);
+            mma(d_tmem, ad, bst, idesc, jj > 0 ? 1u : 0u);
             mma(d_tmem, ad + astep, bst + bstep, idesc, 1u);
             mma(d_tmem, ad + 2 * astep, bst + 2 * bstep, idesc, 1u);
             mma(d_tmem, ad + 3 * astep, bst + 3 * bstep, idesc, 1u);
+            if (C::DROP && jj == t.nlora - 1) commit(lora_full(u & 1u));
             if (jj == njobs - 1) commit(tmem_full(u & 1u));  // this sub-tile's sum is complete
           }
           if (!ok) break;
@@ -696,6 +686,33 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
       }
     };
     bool ok = true;
+    // DROP: keep bits of this thread's row for the 32 tokens of each chunk of a
+    // tile (the next unit with work from `tile` on), and the phases of
+    // lora_full(0), lora_full(1)
+    uint32_t keep[C::DROP ? C::NTT * C::NCHUNK : 1];
+    uint32_t lph = 0;
+    auto keep_words = [&](int tile) {
+      for (; tile < num_tiles; tile += tile_step) {
+        const TileCoord t = coord(tile);
+        if (t.nmain == 0) continue;
+        const int base = t.row0 + warp * 32, end = tile_end(t);
+        if (t.nlora == 0 || base >= args.rows) return;
+#pragma unroll 1
+        for (int i = 0; i < t.nst * C::NCHUNK; ++i) {
+          const int st = i / C::NCHUNK, ch = i % C::NCHUNK;
+          if (ch >= t.half / 16 || (t.only >= 0 && st != t.only)) continue;
+          const int tok = chunk_token(t, st, ch) + lane;
+          if (tok - lane >= end) continue;
+          const uint64_t group = (static_cast<uint64_t>(tok) * args.out_ld + base) / 8;
+          uint32_t word = 0u;
+#pragma unroll 1
+          for (int j = 0; j < 4; ++j) word |= dropout_keep8(args.drop, group + j) << (8 * j);
+          keep[i] = transpose_bits(word, lane);
+        }
+        return;
+      }
+    };
+    if constexpr (C::DROP) keep_words(first_tile);
     for (int tile = first_tile; ok && tile < num_tiles; tile += tile_step, ++iter) {
       const TileCoord t = coord(tile);
       if (C::GROUPED && t.nmain == 0) {
@@ -705,27 +722,36 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
       const int row = t.row0 + qrow;
       const int end = tile_end(t), nchunk = tile_chunks(t), nsub = tile_subs(t);
       auto tok0 = [&](int st, int ch) { return chunk_token(t, st, ch); };
-      // SEP: keep bits of the 32 rows of this warp for token tok0(0, ch) +
-      // lane, evaluated while the tile's MMAs run
-      uint32_t keep[C::SEP ? C::NCHUNK : 1];
-      if constexpr (C::SEP) {
-        const int base = t.row0 + warp * 32;  // rows is a multiple of 64: 32 rows or none
+      if constexpr (C::DROP) {
+        // mask the low-rank sums in place (columns and rows out of range are never stored: as they are)
+        for (int st = 0; t.nlora > 0 && st < nsub; ++st) {
+          const uint32_t acc = (iter * C::NTT + st) & 1u;
+          if (t.only >= 0 && st != t.only) continue;
+          if (!wait_warp(lora_full(acc), (lph >> acc) & 1u)) { ok = false; break; }
+          lph ^= 1u << acc;
+          tc_fence_after();
+          const uint32_t tcol = tmem_base + ((uint32_t)(warp * 32) << 16) + acc * C::ACC_STRIDE;
 #pragma unroll 1
-        for (int ch = 0; ch < nchunk; ++ch) {
-          const int tok = tok0(0, ch) + lane;
-          uint32_t word = 0u;
-          if (t.nlora > 0 && tok < end && base < args.rows) {
-            const uint64_t group = (static_cast<uint64_t>(tok) * args.out_ld + base) / 8;
-#pragma unroll 1
-            for (int j = 0; j < 4; ++j) word |= dropout_keep8(args.drop, group + j) << (8 * j);
+          for (int ch = 0; ch < nchunk && row - lane < args.rows; ++ch) {
+            if (tok0(st, ch) >= end) continue;
+            uint32_t w[32];
+            tmem_ld_32x32b_x32(tcol + ch * 32, w);
+            const uint32_t word = keep[st * C::NCHUNK + ch];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) w[j] = (word >> j) & 1u ? w[j] : 0u;
+            tmem_st_32x32b_x32(tcol + ch * 32, w);
           }
-          keep[ch] = word;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_leader(masked(acc));
         }
+        if (!ok) continue;
+        keep_words(tile + tile_step);  // of the next tile, while this one runs
       }
       float4 *pcol = t.nsplit > 1 ? part_at(t.split, t.tail, qrow) : nullptr;
 #pragma unroll 1
       for (int st = 0; st < C::NTT; ++st) {
-        const uint32_t u = iter * C::USES + st;
+        const uint32_t u = iter * C::NTT + st;
         if (!wait_warp(tmem_full(u & 1u), (u >> 1) & 1u)) { ok = false; break; }
         tc_fence_after();
         if ((t.only >= 0 && st != t.only) || st >= nsub) {  // computed by another unit, or without tokens
@@ -740,19 +766,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
           if (tok0(st, ch) >= end) continue;  // no token in these columns
           uint32_t w[32];
           load_chunk(tcol, ch, w);
-          if constexpr (C::SEP) {
-            if (t.nlora > 0) {  // join the low-rank sum, each element under its keep bit
-              uint32_t l[32];
-              tmem_ld_32x32b_x32(tcol + C::ACC_STRIDE + ch * 32, l);
-              const uint32_t word = keep[ch];
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const uint32_t bits = __shfl_sync(0xFFFFFFFFu, word, j);
-                const float add = (bits >> lane) & 1u ? __uint_as_float(l[j]) * args.drop.factor : 0.0f;
-                w[j] = __float_as_uint(__uint_as_float(w[j]) + add);
-              }
-            }
-          }
           if (t.nsplit == 1) {
             float v[32];
 #pragma unroll
@@ -855,7 +868,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
       pf_jj = -1;
       const int nsup = (t.nmain + C::KSUP - 1) / C::KSUP;
       for (int jj = 0; jj < njobs; ++jj, ++job) {
-        const bool main_job = jj < t.nmain;
+        const bool main_job = C::DROP ? jj >= t.nlora : jj < t.nmain;
+        const int mj = C::DROP ? jj - t.nlora : jj;  // index among the main jobs
         if ((int)(job % C::NGROUPS) != group) continue;
         // this thread's block constant for the job, c' = t8[q] * S (the same
         // fp32 product as the dequantization): its code and scale were loaded
@@ -863,15 +877,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
         uint32_t qv = 0u;
         float sv = 0.0f;  // rows past the weight: c' = 0, the rows decode to zeros
         if (main_job) {
-          if (pf_jj == jj) {
+          if (pf_jj == mj) {
             qv = pf_q;
             sv = pf_s;
           } else {
-            load_consts(t, jj, qv, sv);
+            load_consts(t, mj, qv, sv);
           }
-          if (jj + C::NGROUPS < t.nmain) {  // this group's next job of the tile
-            load_consts(t, jj + C::NGROUPS, pf_q, pf_s);
-            pf_jj = jj + C::NGROUPS;
+          if (mj + C::NGROUPS < t.nmain) {  // this group's next job of the tile
+            load_consts(t, mj + C::NGROUPS, pf_q, pf_s);
+            pf_jj = mj + C::NGROUPS;
           } else {
             pf_jj = -1;
           }
@@ -879,8 +893,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
         const int sa = job % C::SA;
         if (!wait_warp(a_empty(sa), ((job / C::SA) & 1u) ^ 1u)) { ok = false; break; }
         if (main_job) {
-          const uint32_t my_ms = ms + jj / C::KSUP;
-          const int sub = jj % C::KSUP;
+          const uint32_t my_ms = ms + mj / C::KSUP;
+          const int sub = mj % C::KSUP;
           const int sp = my_ms % C::SP;
           if (!wait_warp(p_full(sp), (my_ms / C::SP) & 1u)) { ok = false; break; }
           const uint8_t *pslot = smem + C::OFF_P + sp * C::P_BYTES;
@@ -904,8 +918,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
           __syncwarp();
           if (lane == 0) {  // this sub-job's share of the slot is consumed
             // a short last superjob releases the missing sub-jobs' shares too
-            const int nsub = t.nmain - (jj / C::KSUP) * C::KSUP;
-            const int extra = (jj == t.nmain - 1 && nsub < C::KSUP) ? C::KSUP - nsub : 0;
+            const int nsub = t.nmain - (mj / C::KSUP) * C::KSUP;
+            const int extra = (mj == t.nmain - 1 && nsub < C::KSUP) ? C::KSUP - nsub : 0;
             for (int e = 0; e <= extra; ++e) mbar_arrive(p_empty(sp));
           }
           uint8_t *a_slot = smem + C::OFF_A + sa * C::A_BYTES;

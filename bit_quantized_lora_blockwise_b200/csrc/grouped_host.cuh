@@ -27,12 +27,15 @@ using GroupedFwd1 = GemmCfg<256, A_DEQ_K, L2_A_MN, kPairBkb, kPairSb, kPairSa, k
 using GroupedFwd2 = GemmCfg<256, A_DEQ_K, L2_A_MN, kPair2Bkb, kPair2Sb, kPair2Sa, kPair2Sp, kPair2Npw, true, 2, true>;
 using GroupedBwd1 = GemmCfg<256, A_DEQ_MN, L2_A_K, kPairBkb, kPairSb, kPairSa, kPairSp, kPairNpw, true, 1, true>;
 using GroupedBwd2 = GemmCfg<256, A_DEQ_MN, L2_A_K, kPair2Bkb, kPair2Sb, kPair2Sa, kPair2Sp, kPair2Npw, true, 2, true>;
-using GroupedBwdDrop =
+// the backward with adapter dropout: low-rank step first, masked in TMEM
+using GroupedBwdDrop1 =
     GemmCfg<256, A_DEQ_MN, L2_A_K, kPairBkb, kPairSb, kPairSa, kPairSp, kPairNpw, true, 1, true, true>;
+using GroupedBwdDrop2 =
+    GemmCfg<256, A_DEQ_MN, L2_A_K, kPair2Bkb, kPair2Sb, kPair2Sa, kPair2Sp, kPair2Npw, true, 2, true, true>;
 
 int grouped_pair_slots(int sms) {
   const int n = std::min({resident_pairs<GroupedFwd1>(), resident_pairs<GroupedFwd2>(), resident_pairs<GroupedBwd1>(),
-                          resident_pairs<GroupedBwd2>(), resident_pairs<GroupedBwdDrop>()});
+                          resident_pairs<GroupedBwd2>(), resident_pairs<GroupedBwdDrop1>(), resident_pairs<GroupedBwdDrop2>()});
   return std::min(n, sms / 2);  // 0 without a device: the calls then return before any launch
 }
 
@@ -77,7 +80,7 @@ struct GroupedBwdPlan {
 };
 GroupedBwdPlan plan_grouped_bwd(const GroupedShape &s, int sms) {
   GroupedBwdPlan p{};
-  p.ntt = !s.drop && s.T / s.E >= kGroupedTwoSubtile ? 2 : 1;
+  p.ntt = s.T / s.E >= kGroupedTwoSubtile ? 2 : 1;
   p.slots = grouped_pair_slots(sms);
   p.counters = 2 * p.slots;
   p.part = grouped_part_bytes(p.slots, p.ntt, s.N / 64);
@@ -129,6 +132,9 @@ qlora_status make_dropout(const qlora_dropout_desc *d, DropoutArgs *out) {
 qlora_status run_dropout(const void *x, void *y, int64_t n, int type, const DropoutArgs &d, float factor, int sms,
                          cudaStream_t st) {
   const int grid = grid_for(cdiv(n, 8), 256, sms, 8);
+  // the adapter branch's M o X: kept 16-bit elements as they are
+  if (factor == 1.0f && type != DROP_F32)
+    return launch_pdl(dropout_kernel<DROP_BF16, false>, grid, 256, 0, st, x, y, n, d, factor);
   if (type == DROP_F32) return launch_pdl(dropout_kernel<DROP_F32>, grid, 256, 0, st, x, y, n, d, factor);
   if (type == DROP_F16) return launch_pdl(dropout_kernel<DROP_F16>, grid, 256, 0, st, x, y, n, d, factor);
   return launch_pdl(dropout_kernel<DROP_BF16>, grid, 256, 0, st, x, y, n, d, factor);
@@ -188,7 +194,7 @@ qlora_status grouped_rows(SkinnyKind kind, const void *rows, const void *adapter
                        : run_skinny<false, false, true>(a, p.bn, grid, st);
 }
 
-// dA_e = factor * xm_e^T gs_e and dB_e = (xa_e^T dY_e) * s, every expert's in one launch.
+// dA_e = xm_e^T gs_e and dB_e = s xa_e^T dY_e, every expert's in one launch.
 qlora_status grouped_adapter_grads(const void *xm, const void *dY, const void *gs, const void *xa, const GroupedShape &s,
                                    const GroupArgs &g, void *dA, float a_scale, void *dB, float b_scale,
                                    cudaStream_t st) {
@@ -356,7 +362,8 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
   qlora_status st = QLORA_OK;
 
   // 1) M o X again (never kept from the forward), XA where it was not saved,
-  //    and Gs = s dY B^T, whose launch zeroes the counters
+  //    and Gs = s dY B^T times the dropout factor (dX and dA mask it, nothing
+  //    else), whose launch zeroes the counters
   const void *xin = X;
   if (s.drop) {
     st = run_dropout(X, xm, s.T * s.K, t_f16 ? DROP_F16 : DROP_BF16, drop, 1.0f, sms, cs);
@@ -368,7 +375,7 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
     if (st != QLORA_OK) return st;
     XA = xa_ws;
   }
-  st = grouped_rows(SK_G, dY, B, s, g, gs, scl, nullptr, 0.0f, counters, p.counters, cs);
+  st = grouped_rows(SK_G, dY, B, s, g, gs, scl * drop.factor, nullptr, 0.0f, counters, p.counters, cs);
   if (st != QLORA_OK) return st;
 
   // 2) dX
@@ -382,13 +389,14 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
   grouped_gemm_args(&a, q, scale2, nf4, t8, s, g, s.K, s.N / 64, dX, part, counters);
   a.drop = drop;
   trace_begin(cs);
-  st = s.drop       ? run_grouped_gemm<GroupedBwdDrop>(a, p.slots, cs)
-       : p.ntt == 2 ? run_grouped_gemm<GroupedBwd2>(a, p.slots, cs)
-                    : run_grouped_gemm<GroupedBwd1>(a, p.slots, cs);
+  if (s.drop)
+    st = p.ntt == 2 ? run_grouped_gemm<GroupedBwdDrop2>(a, p.slots, cs) : run_grouped_gemm<GroupedBwdDrop1>(a, p.slots, cs);
+  else
+    st = p.ntt == 2 ? run_grouped_gemm<GroupedBwd2>(a, p.slots, cs) : run_grouped_gemm<GroupedBwd1>(a, p.slots, cs);
   trace_end(cs);
   if (st != QLORA_OK) return st;
 
   // 3) dA and dB "late", as in the dense backward: every operand is complete
   //    when this launch starts and dX is neither read nor written by it
-  return grouped_adapter_grads(xin, dY, gs, XA, s, g, dA, drop.factor, dB, scl, cs);
+  return grouped_adapter_grads(xin, dY, gs, XA, s, g, dA, 1.0f, dB, scl, cs);
 }

@@ -398,6 +398,20 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&v)
       : "memory");
 }
 
+// The store form: 32 registers per thread -> 32 consecutive columns, complete
+// (tcgen05.wait::st) on return.
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+      "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
+      "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]), "r"(taddr)
+      : "memory");
+}
+
 // 32 lanes x 16 consecutive 32-bit columns (tail chunk of a 16-column
 // multiple).
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&v)[16]) {
@@ -499,6 +513,55 @@ __device__ __forceinline__ uint32_t pack_16x2(float lo, float hi, bool f16) {
 __device__ __forceinline__ uint16_t to_16(float v, bool f16) {
   if (f16) return __half_as_ushort(__float2half_rn(v));
   return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+
+// ------------------------------------------------ 32 x 32 warp transposes --
+// A warp holds 32 rows (one per lane) of 32 columns and stores them column by
+// column, rows contiguous: three exchanges between lanes that differ in bit
+// 0, 1 and 2 give lane l the 8 consecutive rows 8 (l / 8) .. + 7 of the
+// columns 8 i + (l & 7), rounded to 16 bits, i = 0..3 (one 16-byte store each).
+__device__ __forceinline__ void rows_to_columns(const float (&v)[32], int lane, bool f16, uint4 (&out)[4]) {
+  const uint32_t sel = lane & 1 ? 0x3276u : 0x5410u;
+  const bool b1 = lane & 2, b2 = lane & 4;
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t own = pack_16x2(v[2 * i], v[2 * i + 1], f16);
+    w[i] = prmt(own, __shfl_xor_sync(0xFFFFFFFFu, own, 1), sel);  // column 2 i + bit 0, two rows
+  }
+  uint32_t x[8][2];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {  // column 4 i + 2 bit 1 + bit 0, four rows
+    const uint32_t own = b1 ? w[2 * i + 1] : w[2 * i];
+    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, b1 ? w[2 * i] : w[2 * i + 1], 2);
+    x[i][0] = b1 ? got : own;
+    x[i][1] = b1 ? own : got;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t own[2], got[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      own[h] = b2 ? x[2 * i + 1][h] : x[2 * i][h];
+      got[h] = __shfl_xor_sync(0xFFFFFFFFu, b2 ? x[2 * i][h] : x[2 * i + 1][h], 4);
+    }
+    out[i] = b2 ? make_uint4(got[0], got[1], own[0], own[1]) : make_uint4(own[0], own[1], got[0], got[1]);
+  }
+}
+
+// Transpose of a 32 x 32 bit matrix, one row (word) per lane: bit j of lane i
+// becomes bit i of lane j. Five exchanges of half words, bytes, ... bits
+// between lanes that differ in one bit.
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t w, int lane) {
+  constexpr uint32_t M[5] = {0x0000FFFFu, 0x00FF00FFu, 0x0F0F0F0Fu, 0x33333333u, 0x55555555u};
+#pragma unroll
+  for (int k = 0; k < 5; ++k) {
+    const int d = 16 >> k;
+    const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, w, d);
+    w = lane & d ? (w & ~M[k]) | ((o >> d) & M[k]) : (w & M[k]) | ((o & M[k]) << d);
+  }
+  return w;
 }
 
 }  // namespace qlora
