@@ -79,6 +79,8 @@
 // of a tile are evaluated while the tile before it runs.
 #pragma once
 
+#include <type_traits>
+
 #include "codec.cuh"
 #include "dropout.cuh"
 #include "groups.cuh"
@@ -198,7 +200,7 @@ struct TileCoord {
   int group;      // expert (0 when dense)
   int end;        // one past the tile's last token
   int nst;        // token sub-tiles of this tile
-  int half;       // columns per CTA half of a sub-tile; an MMA has 2 half columns (pairs)
+  int h0, h1;     // columns per CTA half of sub-tile 0 and 1; an MMA has twice as many (pairs)
 };
 
 // Tile `tile` of a grid of row_tiles x col_tiles tiles of (128 ncta) rows x
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
       t.group = 0;
       t.end = args.cols;
       t.nst = C::NTT;
-      t.half = C::B_ROWS;
+      t.h0 = t.h1 = C::B_ROWS;
       return t;
     } else {
       TileCoord t;
@@ -418,14 +420,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
       const int rt = local / ct_n, ct = local - rt * ct_n;
       t.group = g;
       t.row0 = (rt * C::NCTA + static_cast<int>(rank)) * 128;
-      t.col0 = gt.first[g] + ct * C::TILE_COLS;
-      const int left = gt.first[g + 1] - t.col0;
-      const int ntok = left < C::TILE_COLS ? left : C::TILE_COLS;
-      t.end = t.col0 + ntok;
-      t.nst = ntok > C::BN ? 2 : 1;  // (NTT = 1: never over BN)
-      // columns per sub-tile: a multiple of 64, so that a 32-column chunk of
-      // the epilogue lies in one CTA half
-      t.half = (((ntok + t.nst - 1) / t.nst + 63) / 64) * 32;
+      // the expert's tokens in units of 64, spread evenly over its tiles (a
+      // tile takes some 500 ns per K block however few tokens it has: 600
+      // tokens as 320 + 280, not 512 + 88)
+      const int n = gt.first[g + 1] - gt.first[g], n64 = (n + 63) / 64;
+      const int b64 = static_cast<int>(static_cast<int64_t>(ct) * n64 / ct_n);
+      const int e64 = static_cast<int>(static_cast<int64_t>(ct + 1) * n64 / ct_n);
+      t.col0 = gt.first[g] + b64 * 64;
+      t.end = e64 == n64 ? gt.first[g + 1] : gt.first[g] + e64 * 64;
+      // a sub-tile takes up to 256 columns, in units of 64 so that a 32-column
+      // chunk of the epilogue lies in one CTA half
+      const int u0 = e64 - b64 < 4 ? e64 - b64 : 4;
+      t.h0 = u0 * 32;
+      t.h1 = (e64 - b64 - u0) * 32;
+      t.nst = t.h1 > 0 ? 2 : 1;  // (NTT = 1: never over 4 units)
       t.rc = t.tail * C::NCTA + static_cast<int>(rank);  // counter of a split tile
       t.kb_begin = static_cast<int>((static_cast<int64_t>(t.split) * args.kblocks) / t.nsplit);
       t.nmain = static_cast<int>((static_cast<int64_t>(t.split + 1) * args.kblocks) / t.nsplit) - t.kb_begin;
@@ -438,19 +446,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
     }
   };
 
+  auto half_of = [](const TileCoord &t, int st) { return C::NTT > 1 && st ? t.h1 : t.h0; };
   // first token of the 32 columns of chunk ch of sub-tile st (they never
   // straddle the CTA halves)
   auto chunk_token = [&](const TileCoord &t, int st, int ch) {
     const int c0 = ch * 32;
     if constexpr (C::GROUPED) {
-      const int hi = c0 >= t.half ? 1 : 0;
-      return t.col0 + hi * t.nst * t.half + st * t.half + c0 - hi * t.half;
+      const int h = half_of(t, st), first = t.col0 + (st ? t.h0 : 0);  // (the leader's half)
+      return c0 < h ? first + c0 : first + t.h0 + t.h1 + c0 - h;
     } else {
       return t.col0 + (c0 / C::B_ROWS) * C::CTA_TOK + st * C::B_ROWS + c0 % C::B_ROWS;
     }
   };
   auto tile_end = [&](const TileCoord &t) { return C::GROUPED ? t.end : args.cols; };
-  auto tile_chunks = [&](const TileCoord &t) { return C::GROUPED ? t.half / 16 : C::NCHUNK; };  // with columns
+  auto tile_chunks = [&](const TileCoord &t, int st) { return C::GROUPED ? half_of(t, st) / 16 : C::NCHUNK; };
   auto tile_subs = [&](const TileCoord &t) { return C::GROUPED ? t.nst : C::NTT; };
   // fp32 partials of the split tiles, rows padded to whole 32-column chunks
   // per sub-tile. Partial of split sp of tail tile ti: first float4 of this
@@ -503,7 +512,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
       for (int tile = first_tile; ok && tile < num_tiles; tile += tile_step) {
         const TileCoord t = coord(tile);
         // first token that this CTA loads: its half of every sub-tile, consecutive
-        const int tok = t.col0 + static_cast<int>(rank) * (C::GROUPED ? t.nst * t.half : C::CTA_TOK);
+        const int tok = t.col0 + static_cast<int>(rank) * (C::GROUPED ? t.h0 + t.h1 : C::CTA_TOK);
         const int nbm = (t.nmain + C::BKB - 1) / C::BKB;
         for (int i = 0; i < nbm + t.nlora; ++i, ++bs) {
           // stage st: the main ones, then the low-rank ones (DROP: low-rank first)
@@ -588,73 +597,105 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
         else tc_commit(bar);
       };
       const uint32_t a_base = sbase + C::OFF_A, b_base = sbase + C::OFF_B;
-      uint32_t job = 0, bs = 0, iter = 0, mph = 0;  // mph: phases of masked(0), masked(1)
-      bool ok = true;
+      uint32_t iter = 0, mph = 0;  // mph: phases of masked(0), masked(1)
+      bool masking = false;        // DROP: the next main job waits for them
+      int sa = 0, sb = 0;          // ring slots and phases of the next job
+      uint32_t pa = 0, pb = 0;
+      // Whether the next job's operands were seen ready: polled before the
+      // present job's MMAs are issued, so that the latency of the poll (some
+      // 100 clocks each) hides behind them.
+      bool a_ready = false, b_ready = false;
+      bool ok = true, any = false;
       for (int tile = first_tile; ok && tile < num_tiles; tile += tile_step, ++iter) {
         const TileCoord t = coord(tile);
-        const int njobs = t.nmain + t.nlora;
-        if (C::GROUPED && njobs == 0) {  // nothing to do and no accumulator used
+        if (C::GROUPED && t.nmain + t.nlora == 0) {  // nothing to do and no accumulator used
           --iter;
           continue;
         }
-        // accumulator use u = iter * NTT + sub-tile: accumulator u & 1, phase u >> 1
+        any = true;
+        // accumulator use u = iter * NTT + sub-tile: accumulator u & 1, phase u >> 1.
+        // A sub-tile this unit leaves to another, or without tokens, is not
+        // active: its accumulator's phases still advance (nothing is written).
         const uint32_t u0 = iter * C::NTT;
-        const int half = C::GROUPED ? t.half : C::B_ROWS;
-        const uint32_t ncols = C::GROUPED ? static_cast<uint32_t>(2 * t.half) >> 3 << 17 : 0u;  // MMA N field
-        int sa = job % C::SA;
-        uint32_t pa = (job / C::SA) & 1u;
-        for (int jj = 0; jj < njobs; ++jj, ++job) {
-          const bool main_job = C::DROP ? jj >= t.nlora : jj < t.nmain;
-          const int sub = main_job ? jj % C::BKB : 0;  // K block within the token stage
-          const bool last_of_stage = !main_job || sub == C::BKB - 1 || jj == t.nmain - 1;
-          const int sb = bs % C::SB;
-          if (sub == 0 && !wait_full(b_full(sb), (bs / C::SB) & 1u)) { ok = false; break; }
-          if (!wait_full(a_full(sa), pa)) { ok = false; break; }
+        bool active[C::NTT];
+        uint32_t ncols[C::NTT], d_tmem[C::NTT];
+#pragma unroll
+        for (int st = 0; st < C::NTT; ++st) {
+          active[st] = !(t.only >= 0 && st != t.only) && !(C::GROUPED && st >= t.nst);
+          ncols[st] = C::GROUPED ? static_cast<uint32_t>(2 * half_of(t, st)) >> 3 << 17 : 0u;  // MMA N field
+          d_tmem[st] = tmem_base + ((u0 + st) & 1u) * C::ACC_STRIDE;
+        }
+        const uint32_t b_sub = (C::GROUPED ? t.h0 : C::B_ROWS) * 128 >> 4;  // sub-tile 1's tokens of a stage
+        // One job: `first` and `last` of its tile; `sub`: K block within the token stage.
+        auto step = [&](auto main_kind, bool first, bool last, int sub, bool last_of_stage) {
+          constexpr bool MAIN = decltype(main_kind)::value;
+          if (sub == 0 && !b_ready && !wait_full(b_full(sb), pb)) return false;
+          if (!a_ready && !wait_full(a_full(sa), pa)) return false;
           tc_fence_after();
-          const bool a_mn = main_job ? C::A_MN : (C::L2 == L2_A_MN);
-          const uint64_t ad = (a_mn ? DM : DK) | (((a_base + sa * C::A_BYTES) >> 4) & 0x3FFFu);
+          const int na = sa + 1 == C::SA ? 0 : sa + 1, nb = sb + 1 == C::SB ? 0 : sb + 1;
+          a_ready = mbar_test(a_full(na), na ? pa : pa ^ 1u);
+          b_ready = last_of_stage && mbar_test(b_full(nb), nb ? pb : pb ^ 1u);
+          constexpr bool A_MN = MAIN ? C::A_MN : (C::L2 == L2_A_MN);
+          const uint64_t ad = (A_MN ? DM : DK) | (((a_base + sa * C::A_BYTES) >> 4) & 0x3FFFu);
           const uint64_t bd = DK | (((b_base + sb * C::B_BYTES + sub * C::KB_BYTES) >> 4) & 0x3FFFu);
-          const uint32_t astep = a_mn ? 2048u >> 4 : 32u >> 4, bstep = 32u >> 4;
-          const uint32_t idesc = (main_job ? ID_MAIN : ID_LORA) | ncols;
+          constexpr uint32_t astep = A_MN ? 2048u >> 4 : 32u >> 4, bstep = 32u >> 4;
 #pragma unroll
           for (int st = 0; st < C::NTT; ++st) {
-            const uint32_t u = u0 + st;
-            if (jj == 0) {  // the accumulator's previous tile has been drained
-              if (!wait_full(tmem_empty(u & 1u), ((u >> 1) & 1u) ^ 1u)) { ok = false; break; }
+            const uint32_t acc = (u0 + st) & 1u;
+            if (first) {  // the accumulator's previous tile has been drained
+              if (!wait_full(tmem_empty(acc), (((u0 + st) >> 1) & 1u) ^ 1u)) return false;
               tc_fence_after();
             }
-            if ((t.only >= 0 && st != t.only) || (C::GROUPED && st >= t.nst)) {
-              // a sub-tile this unit leaves to another, or without tokens: its
-              // accumulator's phases still advance (nothing to drain, nothing written)
-              if (jj == njobs - 1) commit(tmem_full(u & 1u));
-              continue;
-            }
-            if (C::DROP && t.nlora > 0 && jj == t.nlora) {  // the low-rank sum has been masked
-              if (!wait_full(masked(u & 1u), (mph >> (u & 1u)) & 1u)) { ok = false; break; }
-              mph ^= 1u << (u & 1u);
+            if (!active[st]) continue;
+            if (C::DROP && MAIN && !first && masking) {  // the first main job: the low-rank sum has been masked
+              if (!wait_full(masked(acc), (mph >> acc) & 1u)) return false;
+              mph ^= 1u << acc;
               tc_fence_after();
             }
-            const uint32_t d_tmem = tmem_base + (u & 1u) * C::ACC_STRIDE;
-            const uint64_t bst = bd + ((st * half * 128) >> 4);  // sub-tile st's tokens of the stage
-            mma(d_tmem, ad, bst, idesc, jj > 0 ? 1u : 0u);
-            mma(d_tmem, ad + astep, bst + bstep, idesc, 1u);
-            mma(d_tmem, ad + 2 * astep, bst + 2 * bstep, idesc, 1u);
-            mma(d_tmem, ad + 3 * astep, bst + 3 * bstep, idesc, 1u);
-            if (C::DROP && jj == t.nlora - 1) commit(lora_full(u & 1u));
-            if (jj == njobs - 1) commit(tmem_full(u & 1u));  // this sub-tile's sum is complete
+            const uint32_t idesc = (MAIN ? ID_MAIN : ID_LORA) | ncols[st];
+            const uint64_t bst = bd + st * b_sub;
+            mma(d_tmem[st], ad, bst, idesc, first ? 0u : 1u);
+            mma(d_tmem[st], ad + astep, bst + bstep, idesc, 1u);
+            mma(d_tmem[st], ad + 2 * astep, bst + 2 * bstep, idesc, 1u);
+            mma(d_tmem[st], ad + 3 * astep, bst + 3 * bstep, idesc, 1u);
+            if (last) commit(tmem_full(acc));  // this sub-tile's sum is complete
           }
-          if (!ok) break;
+          masking = false;
           commit(a_empty(sa));
+          sa = na;
+          pa ^= na ? 0u : 1u;
           if (last_of_stage) {
             commit(b_empty(sb));
-            ++bs;
+            sb = nb;
+            pb ^= nb ? 0u : 1u;
           }
-          if (++sa == C::SA) { sa = 0; pa ^= 1u; }
+          return true;
+        };
+        if constexpr (C::DROP) {
+          for (int l = 0; ok && l < t.nlora; ++l) ok = step(std::false_type{}, l == 0, false, 0, true);
+          if (ok && t.nlora > 0) {
+            masking = true;
+#pragma unroll
+            for (int st = 0; st < C::NTT; ++st)
+              if (active[st]) commit(lora_full((u0 + st) & 1u));
+          }
         }
+        const int nl = C::DROP ? 0 : t.nlora;  // low-rank jobs that follow
+        const bool first0 = !C::DROP || t.nlora == 0;
+        for (int j = 0; ok && j < t.nmain; ++j) {
+          const int sub = C::BKB == 1 ? 0 : j % C::BKB;
+          const bool last = j == t.nmain - 1;
+          ok = step(std::true_type{}, first0 && j == 0, last && nl == 0, sub, sub == C::BKB - 1 || last);
+        }
+        for (int l = 0; ok && l < nl; ++l) ok = step(std::false_type{}, false, l == nl - 1, 0, true);
+        if (!ok) break;
+#pragma unroll
+        for (int st = 0; st < C::NTT; ++st)
+          if (!active[st]) commit(tmem_full((u0 + st) & 1u));
       }
       // all MMAs issued by this thread have completed once drain_bar flips
       // (a grouped launch may leave a pair without units)
-      if (!C::GROUPED || job > 0) {
+      if (!C::GROUPED || any) {
         if constexpr (C::PAIR) tc_commit_pair(drain_bar, 0x1);
         else tc_commit(drain_bar);
         const unsigned long long t0 = globaltimer_ns();
@@ -700,7 +741,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
 #pragma unroll 1
         for (int i = 0; i < t.nst * C::NCHUNK; ++i) {
           const int st = i / C::NCHUNK, ch = i % C::NCHUNK;
-          if (ch >= t.half / 16 || (t.only >= 0 && st != t.only)) continue;
+          if (ch >= tile_chunks(t, st) || (t.only >= 0 && st != t.only)) continue;
           const int tok = chunk_token(t, st, ch) + lane;
           if (tok - lane >= end) continue;
           const uint64_t group = (static_cast<uint64_t>(tok) * args.out_ld + base) / 8;
@@ -720,7 +761,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
         continue;
       }
       const int row = t.row0 + qrow;
-      const int end = tile_end(t), nchunk = tile_chunks(t), nsub = tile_subs(t);
+      const int end = tile_end(t), nsub = tile_subs(t);
       auto tok0 = [&](int st, int ch) { return chunk_token(t, st, ch); };
       if constexpr (C::DROP) {
         // mask the low-rank sums in place (columns and rows out of range are never stored: as they are)
@@ -732,7 +773,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
           tc_fence_after();
           const uint32_t tcol = tmem_base + ((uint32_t)(warp * 32) << 16) + acc * C::ACC_STRIDE;
 #pragma unroll 1
-          for (int ch = 0; ch < nchunk && row - lane < args.rows; ++ch) {
+          for (int ch = 0; ch < tile_chunks(t, st) && row - lane < args.rows; ++ch) {
             if (tok0(st, ch) >= end) continue;
             uint32_t w[32];
             tmem_ld_32x32b_x32(tcol + ch * 32, w);
@@ -762,7 +803,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
         }
         const uint32_t tcol = tmem_base + ((uint32_t)(warp * 32) << 16) + (u & 1u) * C::ACC_STRIDE;
 #pragma unroll 1
-        for (int ch = 0; ch < nchunk; ++ch) {
+        for (int ch = 0; ch < tile_chunks(t, st); ++ch) {
           if (tok0(st, ch) >= end) continue;  // no token in these columns
           uint32_t w[32];
           load_chunk(tcol, ch, w);
@@ -834,64 +875,53 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
     const int p = (pw & 3) * 32 + lane;  // 0..127: the tile row this thread decodes
     const uint32_t a_off = (C::ASRC == A_DEQ_K) ? p * 128 : (p >> 6) * 8192 + (p & 63) * 128;
     const uint32_t swz = p & 7;
-    uint32_t job = 0, ms = 0;  // ms: superjob counter at the start of the tile
+    // This group takes every NGROUPS-th job of the CTA: `next` is the index of
+    // its next job within the tile at hand, (sa, pa) that job's A slot and
+    // phase, ms the superjobs before the tile. The loop is bound by the integer
+    // pipe, of which the lookups need some 190 instructions a job and thread,
+    // so what can be formed once per tile or carried along is.
+    int next = group, sa = group;
+    uint32_t pa = 0, ms = 0;
     bool ok = true;
-    // the 8-bit code and second-level scale of this thread's block in main
-    // job jj of tile t (0 and 0.0 past the weight)
-    auto load_consts = [&](const TileCoord &t, int jj, uint32_t &qv, float &sv) {
-      int64_t n, kblk;  // W row and 64-block of this thread's codes
-      bool valid;
-      if (C::ASRC == A_DEQ_K) {
-        n = t.row0 + p;
-        kblk = t.kb_begin + jj;
-        valid = n < args.rows;
-      } else {
-        n = static_cast<int64_t>(t.kb_begin + jj) * 64 + (p & 63);
-        kblk = t.row0 / 64 + (p >> 6);
-        valid = kblk < args.wkb;
-      }
-      qv = 0u;
-      sv = 0.0f;
-      if (valid) {
-        if constexpr (C::GROUPED) n += static_cast<int64_t>(t.group) * args.expert_rows;
-        const int64_t b = n * args.wkb + kblk;
-        qv = __ldg(args.q + b);
-        sv = __ldg(args.scale2 + (b >> 8));
-      }
-    };
-    int pf_jj = -1;  // main job of the current tile whose constants are in pf_q, pf_s
-    uint32_t pf_q = 0u;
-    float pf_s = 0.0f;
     for (int tile = first_tile; ok && tile < num_tiles; tile += tile_step) {
       const TileCoord t = coord(tile);
       const int njobs = t.nmain + t.nlora;
-      pf_jj = -1;
-      const int nsup = (t.nmain + C::KSUP - 1) / C::KSUP;
-      for (int jj = 0; jj < njobs; ++jj, ++job) {
-        const bool main_job = C::DROP ? jj >= t.nlora : jj < t.nmain;
-        const int mj = C::DROP ? jj - t.nlora : jj;  // index among the main jobs
-        if ((int)(job % C::NGROUPS) != group) continue;
-        // this thread's block constant for the job, c' = t8[q] * S (the same
-        // fp32 product as the dequantization): its code and scale were loaded
-        // one of this group's jobs ahead (or here, for a tile's first jobs)
-        uint32_t qv = 0u;
-        float sv = 0.0f;  // rows past the weight: c' = 0, the rows decode to zeros
-        if (main_job) {
-          if (pf_jj == mj) {
-            qv = pf_q;
-            sv = pf_s;
-          } else {
-            load_consts(t, mj, qv, sv);
-          }
-          if (mj + C::NGROUPS < t.nmain) {  // this group's next job of the tile
-            load_consts(t, mj + C::NGROUPS, pf_q, pf_s);
-            pf_jj = mj + C::NGROUPS;
-          } else {
-            pf_jj = -1;
-          }
+      const int nl = C::DROP ? t.nlora : 0;  // low-rank jobs before the main ones
+      // Constants of this thread's block in main job mj: its 8-bit code at
+      // q[b0 + mj bstep] and the second-level scale (0 and 0.0 past the weight:
+      // c' = 0, the rows decode to zeros).
+      int64_t b0, bstep;
+      bool valid;
+      if (C::ASRC == A_DEQ_K) {
+        const int64_t n = t.row0 + p;
+        valid = n < args.rows;
+        b0 = ((C::GROUPED ? static_cast<int64_t>(t.group) * args.expert_rows : 0) + n) * args.wkb + t.kb_begin;
+        bstep = 1;
+      } else {
+        const int64_t n = static_cast<int64_t>(t.kb_begin) * 64 + (p & 63), kblk = t.row0 / 64 + (p >> 6);
+        valid = kblk < args.wkb;
+        b0 = ((C::GROUPED ? static_cast<int64_t>(t.group) * args.expert_rows : 0) + n) * args.wkb + kblk;
+        bstep = 64 * args.wkb;
+      }
+      auto load_consts = [&](int mj, uint32_t &qv, float &sv) {
+        qv = 0u;
+        sv = 0.0f;
+        if (valid && mj < t.nmain) {
+          const int64_t b = b0 + mj * bstep;
+          qv = __ldg(args.q + b);
+          sv = __ldg(args.scale2 + (b >> 8));
         }
-        const int sa = job % C::SA;
-        if (!wait_warp(a_empty(sa), ((job / C::SA) & 1u) ^ 1u)) { ok = false; break; }
+      };
+      // loaded one of this group's jobs ahead (a tile's first ones here)
+      uint32_t qv = 0u;
+      float sv = 0.0f;
+      const int first_mj = next >= nl ? next - nl : next - nl + ((nl - next + C::NGROUPS - 1) / C::NGROUPS) * C::NGROUPS;
+      load_consts(first_mj, qv, sv);
+      int jj = next;
+      for (; jj < njobs; jj += C::NGROUPS) {
+        const int mj = jj - nl;  // index among the main jobs
+        const bool main_job = mj >= 0 && mj < t.nmain;
+        if (!wait_warp(a_empty(sa), pa ^ 1u)) { ok = false; break; }
         if (main_job) {
           const uint32_t my_ms = ms + mj / C::KSUP;
           const int sub = mj % C::KSUP;
@@ -906,24 +936,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
           if (C::ASRC == A_DEQ_K) {  // [128 rows][KSUP x 32 B]
             const uint32_t x = p & 7;
             p_off0 = p * (32 * C::KSUP) + (((2 * sub) ^ x) << 4);
-            p_off1 = p * (32 * C::KSUP) + (((2 * sub + 1) ^ x) << 4);
+            p_off1 = p_off0 ^ 16u;
           } else {  // [KSUP x 64 rows][2 x 32 B]
             const uint32_t row = sub * 64 + (p & 63), x = (row >> 1) & 3, c0 = 2 * (p >> 6);
             p_off0 = row * 64 + ((c0 ^ x) << 4);
-            p_off1 = row * 64 + (((c0 + 1) ^ x) << 4);
+            p_off1 = p_off0 ^ 16u;
           }
+          // c' = t8[q] * S: the same fp32 product as the dequantization
           const float cp = __fmul_rn(reinterpret_cast<const float *>(smem + C::OFF_T8)[qv], sv);
           const uint4 w0 = *reinterpret_cast<const uint4 *>(pslot + p_off0);
           const uint4 w1 = *reinterpret_cast<const uint4 *>(pslot + p_off1);
-          __syncwarp();
-          if (lane == 0) {  // this sub-job's share of the slot is consumed
-            // a short last superjob releases the missing sub-jobs' shares too
-            const int nsub = t.nmain - (mj / C::KSUP) * C::KSUP;
-            const int extra = (mj == t.nmain - 1 && nsub < C::KSUP) ? C::KSUP - nsub : 0;
-            for (int e = 0; e <= extra; ++e) mbar_arrive(p_empty(sp));
-          }
-          uint8_t *a_slot = smem + C::OFF_A + sa * C::A_BYTES;
-          // out-of-range rows decode with c' = 0 -> zeros
+          load_consts(mj + C::NGROUPS, qv, sv);
+          uint8_t *a_slot = smem + C::OFF_A + sa * C::A_BYTES + a_off;
           const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
           float L[16];  // NF4 levels, re-read each job (shared-memory broadcast) to spare registers
 #pragma unroll
@@ -939,14 +963,30 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
           for (int c = 0; c < 8; ++c) {
             uint32_t o[4];
             nf4_lookup8(P, words[c], o);
-            *reinterpret_cast<uint4 *>(a_slot + a_off + ((c ^ swz) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(a_slot + ((c ^ swz) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
           fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            arrive_leader(a_full(sa));
+            // this sub-job's share of the code slot is consumed; a short last
+            // superjob releases the missing sub-jobs' shares too
+            mbar_arrive(p_empty(sp));
+            if (mj == t.nmain - 1)
+              for (int e = sub + 1; e < C::KSUP; ++e) mbar_arrive(p_empty(sp));
+          }
+        } else {
+          __syncwarp();
+          if (lane == 0) arrive_leader(a_full(sa));
         }
-        __syncwarp();
-        if (lane == 0) arrive_leader(a_full(sa));
+        sa += C::NGROUPS;
+        if (sa >= C::SA) {
+          sa -= C::SA;
+          pa ^= 1u;
+        }
       }
-      ms += nsup;
+      next = jj - njobs;
+      ms += (t.nmain + C::KSUP - 1) / C::KSUP;
     }
   }
 
@@ -966,11 +1006,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
   // four epilogue warps the same 4 x 256 x 256 partials took 26 us.)
   if (*s_last) {
     const TileCoord t = coord(first_tile);
-    const int end = tile_end(t), nchunk = tile_chunks(t), nsub = tile_subs(t);
+    const int end = tile_end(t), nsub = tile_subs(t);
     for (int i = warp; i < 4 * C::NTT * C::NCHUNK; i += C::WARPS) {
       const int quad = i & 3, pc = i >> 2, st = pc / C::NCHUNK, ch = pc % C::NCHUNK;
       const int tok = chunk_token(t, st, ch);
-      if (st >= nsub || ch >= nchunk || tok >= end) continue;  // no columns there
+      if (st >= nsub || ch >= tile_chunks(t, st) || tok >= end) continue;  // no columns there
       float v[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = 0.0f;
