@@ -148,6 +148,12 @@ struct GemmCfg {
   static_assert(CTA_TOK <= 256, "a TMA box spans at most 256 tokens");
   static constexpr bool A_MN = ASRC_ == A_DEQ_MN;
   static constexpr int NGROUPS = NPW_ / 4;
+  // One ring for both operands: a job's tokens and decoded weights share a
+  // stage, one full barrier and one release. The MMA thread's work per job
+  // (its instructions are fetched anew each time, beside the dequant warps'
+  // long loop) sets the pace of the 256-token tiles: two rings cost it two
+  // waits and two commits, 850 clocks a job against XXX.
+  static constexpr bool ONE_RING = BKB_ == 1 && SA_ == SB_;
   static_assert(NPW_ % 4 == 0 && NPW_ >= 4 && SP_ >= 2, "producer groups of 4 warps and a packed-code ring");
   // (a 16-warp, 3-slot configuration timed out on B200: every producer group
   // needs a slot of its own plus a spare, or the groups wait on each other)
@@ -159,10 +165,10 @@ struct GemmCfg {
   static constexpr int KB_BYTES = CTA_TOK * BK * 2;  // one K block of this CTA's tokens
   static constexpr int B_BYTES = KB_BYTES * BKB;
   // P slot: the packed codes of KSUP consecutive 64-deep K blocks of the
-  // 128-row weight tile (128 contiguous bytes per weight row: forward;
-  // 64 bytes of 4 x 64 rows: backward), by TMA, shared by KSUP consecutive
+  // 128-row weight tile (32 KSUP contiguous bytes per weight row: forward;
+  // 64 bytes of KSUP x 64 rows: backward), by TMA, shared by KSUP consecutive
   // MMA jobs. (The block constants come from q and scale2 directly.)
-  static constexpr int KSUP = 4;
+  static constexpr int KSUP = NTT_ == 2 ? 2 : 4;
   static constexpr int PK_BYTES = 4096 * KSUP;
   static constexpr int P_BYTES = PK_BYTES;
   static constexpr int OFF_B = 0;
@@ -280,8 +286,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
   const uint32_t bar0 = sbase + C::OFF_BAR;
   auto b_full = [&](int s) { return bar0 + 8u * s; };
   auto b_empty = [&](int s) { return bar0 + 8u * (C::SB + s); };
-  auto a_full = [&](int s) { return bar0 + 8u * (2 * C::SB + s); };
-  auto a_empty = [&](int s) { return bar0 + 8u * (2 * C::SB + C::SA + s); };
+  auto a_full = [&](int s) { return bar0 + 8u * (C::ONE_RING ? s : 2 * C::SB + s); };
+  auto a_empty = [&](int s) { return bar0 + 8u * (C::ONE_RING ? C::SB + s : 2 * C::SB + C::SA + s); };
   auto p_full = [&](int s) { return bar0 + 8u * (2 * C::SB + 2 * C::SA + s); };
   auto p_empty = [&](int s) { return bar0 + 8u * (2 * C::SB + 2 * C::SA + C::SP + s); };
   constexpr int TB = 2 * C::SB + 2 * C::SA + 2 * C::SP;
@@ -296,10 +302,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::SB; ++s) {
-      mbar_init(b_full(s), 1);
+      mbar_init(b_full(s), C::ONE_RING ? 1 + C::GROUP_ARRIVALS : 1);
       mbar_init(b_empty(s), 1);
     }
-    for (int s = 0; s < C::SA; ++s) {
+    for (int s = 0; s < C::SA && !C::ONE_RING; ++s) {
       mbar_init(a_full(s), C::GROUP_ARRIVALS);
       mbar_init(a_empty(s), 1);
     }
@@ -532,7 +538,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
             wait_prior();  // B2 is the previous launch's output
             const int lk = st - nbm;
             const int sa = job % C::SA;
-            if (!mbar_wait(a_empty(sa), ((job / C::SA) & 1u) ^ 1u, s_abort)) { ok = false; break; }
+            if (!C::ONE_RING && !mbar_wait(a_empty(sa), ((job / C::SA) & 1u) ^ 1u, s_abort)) { ok = false; break; }
             const uint32_t a_dst = sbase + C::OFF_A + sa * C::A_BYTES;
             if (rank == 0) mbar_arrive_expect_tx(b_full(sb), C::LORA_TX);
             load(b_dst, &args.tm_b2, b_full(sb), lk * 64, tok);
@@ -598,13 +604,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
       };
       const uint32_t a_base = sbase + C::OFF_A, b_base = sbase + C::OFF_B;
       uint32_t iter = 0, mph = 0;  // mph: phases of masked(0), masked(1)
-      bool masking = false;        // DROP: the next main job waits for them
       int sa = 0, sb = 0;          // ring slots and phases of the next job
       uint32_t pa = 0, pb = 0;
-      // Whether the next job's operands were seen ready: polled before the
-      // present job's MMAs are issued, so that the latency of the poll (some
-      // 100 clocks each) hides behind them.
-      bool a_ready = false, b_ready = false;
       bool ok = true, any = false;
       for (int tile = first_tile; ok && tile < num_tiles; tile += tile_step, ++iter) {
         const TileCoord t = coord(tile);
@@ -626,72 +627,73 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
           d_tmem[st] = tmem_base + ((u0 + st) & 1u) * C::ACC_STRIDE;
         }
         const uint32_t b_sub = (C::GROUPED ? t.h0 : C::B_ROWS) * 128 >> 4;  // sub-tile 1's tokens of a stage
-        // One job: `first` and `last` of its tile; `sub`: K block within the token stage.
-        auto step = [&](auto main_kind, bool first, bool last, int sub, bool last_of_stage) {
-          constexpr bool MAIN = decltype(main_kind)::value;
-          if (sub == 0 && !b_ready && !wait_full(b_full(sb), pb)) return false;
-          if (!a_ready && !wait_full(a_full(sa), pa)) return false;
-          tc_fence_after();
-          const int na = sa + 1 == C::SA ? 0 : sa + 1, nb = sb + 1 == C::SB ? 0 : sb + 1;
-          a_ready = mbar_test(a_full(na), na ? pa : pa ^ 1u);
-          b_ready = last_of_stage && mbar_test(b_full(nb), nb ? pb : pb ^ 1u);
+        uint32_t accum = 0u;  // 0: the accumulators' first MMAs overwrite them
+        // n jobs of a kind (main, low-rank)
+        auto run = [&](auto kind, int n) -> bool {
+          constexpr bool MAIN = decltype(kind)::value;
           constexpr bool A_MN = MAIN ? C::A_MN : (C::L2 == L2_A_MN);
-          const uint64_t ad = (A_MN ? DM : DK) | (((a_base + sa * C::A_BYTES) >> 4) & 0x3FFFu);
-          const uint64_t bd = DK | (((b_base + sb * C::B_BYTES + sub * C::KB_BYTES) >> 4) & 0x3FFFu);
           constexpr uint32_t astep = A_MN ? 2048u >> 4 : 32u >> 4, bstep = 32u >> 4;
+#pragma unroll 1
+          for (int j = 0; j < n; ++j) {
+            const int sub = MAIN && C::BKB > 1 ? j % C::BKB : 0;  // K block within the token stage
+            if (sub == 0 && !wait_full(b_full(sb), pb)) return false;
+            if (!C::ONE_RING && !wait_full(a_full(sa), pa)) return false;
+            tc_fence_after();
+            const uint64_t ad = (A_MN ? DM : DK) | ((a_base + sa * C::A_BYTES) >> 4);
+            const uint64_t bd = DK | ((b_base + sb * C::B_BYTES + sub * C::KB_BYTES) >> 4);
 #pragma unroll
-          for (int st = 0; st < C::NTT; ++st) {
-            const uint32_t acc = (u0 + st) & 1u;
-            if (first) {  // the accumulator's previous tile has been drained
-              if (!wait_full(tmem_empty(acc), (((u0 + st) >> 1) & 1u) ^ 1u)) return false;
-              tc_fence_after();
+            for (int st = 0; st < C::NTT; ++st) {
+              if (C::NTT > 1 && !active[st]) continue;
+              const uint32_t idesc = (MAIN ? ID_MAIN : ID_LORA) | ncols[st];
+              const uint64_t bst = bd + st * b_sub;
+              mma(d_tmem[st], ad, bst, idesc, accum);
+              mma(d_tmem[st], ad + astep, bst + bstep, idesc, 1u);
+              mma(d_tmem[st], ad + 2 * astep, bst + 2 * bstep, idesc, 1u);
+              mma(d_tmem[st], ad + 3 * astep, bst + 3 * bstep, idesc, 1u);
             }
-            if (!active[st]) continue;
-            if (C::DROP && MAIN && !first && masking) {  // the first main job: the low-rank sum has been masked
-              if (!wait_full(masked(acc), (mph >> acc) & 1u)) return false;
-              mph ^= 1u << acc;
-              tc_fence_after();
+            accum = 1u;
+            if (!C::ONE_RING) {
+              commit(a_empty(sa));
+              if (++sa == C::SA) {
+                sa = 0;
+                pa ^= 1u;
+              }
             }
-            const uint32_t idesc = (MAIN ? ID_MAIN : ID_LORA) | ncols[st];
-            const uint64_t bst = bd + st * b_sub;
-            mma(d_tmem[st], ad, bst, idesc, first ? 0u : 1u);
-            mma(d_tmem[st], ad + astep, bst + bstep, idesc, 1u);
-            mma(d_tmem[st], ad + 2 * astep, bst + 2 * bstep, idesc, 1u);
-            mma(d_tmem[st], ad + 3 * astep, bst + 3 * bstep, idesc, 1u);
-            if (last) commit(tmem_full(acc));  // this sub-tile's sum is complete
-          }
-          masking = false;
-          commit(a_empty(sa));
-          sa = na;
-          pa ^= na ? 0u : 1u;
-          if (last_of_stage) {
-            commit(b_empty(sb));
-            sb = nb;
-            pb ^= nb ? 0u : 1u;
+            if (!MAIN || sub == C::BKB - 1 || j == n - 1) {  // the token stage is read
+              commit(b_empty(sb));
+              if (++sb == C::SB) {
+                sb = 0;
+                pb ^= 1u;
+              }
+              if (C::ONE_RING) sa = sb;
+            }
           }
           return true;
         };
-        if constexpr (C::DROP) {
-          for (int l = 0; ok && l < t.nlora; ++l) ok = step(std::false_type{}, l == 0, false, 0, true);
-          if (ok && t.nlora > 0) {
-            masking = true;
 #pragma unroll
-            for (int st = 0; st < C::NTT; ++st)
-              if (active[st]) commit(lora_full((u0 + st) & 1u));
+        for (int st = 0; st < C::NTT; ++st)  // the accumulators' previous tile has been drained
+          ok = ok && wait_full(tmem_empty((u0 + st) & 1u), (((u0 + st) >> 1) & 1u) ^ 1u);
+        if (!ok) break;
+        tc_fence_after();
+        if (C::DROP && t.nlora > 0) {
+          if (!run(std::false_type{}, t.nlora)) { ok = false; break; }
+#pragma unroll
+          for (int st = 0; st < C::NTT; ++st)
+            if (active[st]) commit(lora_full((u0 + st) & 1u));
+#pragma unroll
+          for (int st = 0; st < C::NTT; ++st) {  // the low-rank sums have been masked
+            const uint32_t acc = (u0 + st) & 1u;
+            if (!active[st]) continue;
+            ok = ok && wait_full(masked(acc), (mph >> acc) & 1u);
+            mph ^= 1u << acc;
           }
+          if (!ok) break;
+          tc_fence_after();
         }
-        const int nl = C::DROP ? 0 : t.nlora;  // low-rank jobs that follow
-        const bool first0 = !C::DROP || t.nlora == 0;
-        for (int j = 0; ok && j < t.nmain; ++j) {
-          const int sub = C::BKB == 1 ? 0 : j % C::BKB;
-          const bool last = j == t.nmain - 1;
-          ok = step(std::true_type{}, first0 && j == 0, last && nl == 0, sub, sub == C::BKB - 1 || last);
-        }
-        for (int l = 0; ok && l < nl; ++l) ok = step(std::false_type{}, false, l == nl - 1, 0, true);
+        ok = run(std::true_type{}, t.nmain) && (C::DROP || run(std::false_type{}, t.nlora));
         if (!ok) break;
 #pragma unroll
-        for (int st = 0; st < C::NTT; ++st)
-          if (!active[st]) commit(tmem_full((u0 + st) & 1u));
+        for (int st = 0; st < C::NTT; ++st) commit(tmem_full((u0 + st) & 1u));  // the tile's sums are complete
       }
       // all MMAs issued by this thread have completed once drain_bar flips
       // (a grouped launch may leave a pair without units)
@@ -928,13 +930,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
           const int sp = my_ms % C::SP;
           if (!wait_warp(p_full(sp), (my_ms / C::SP) & 1u)) { ok = false; break; }
           const uint8_t *pslot = smem + C::OFF_P + sp * C::P_BYTES;
-          // The codes arrive swizzled (TMA 128-byte swizzle on 128-byte rows
-          // for the forward, 64-byte swizzle on 64-byte rows for the
-          // backward): 16-byte chunk c of a row sits at c ^ (row bits), so
+          // The codes arrive swizzled (TMA 128-byte swizzle on 128-byte rows,
+          // 64-byte swizzle on 64-byte rows): 16-byte chunk c of a row sits at c ^ (row bits), so
           // the 8 threads of each quarter-warp read 8 different bank groups.
           uint32_t p_off0, p_off1;
           if (C::ASRC == A_DEQ_K) {  // [128 rows][KSUP x 32 B]
-            const uint32_t x = p & 7;
+            const uint32_t x = C::KSUP == 4 ? p & 7 : (p >> 1) & 3;
             p_off0 = p * (32 * C::KSUP) + (((2 * sub) ^ x) << 4);
             p_off1 = p_off0 ^ 16u;
           } else {  // [KSUP x 64 rows][2 x 32 B]

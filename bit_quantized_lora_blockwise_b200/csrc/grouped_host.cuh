@@ -334,7 +334,7 @@ qlora_status grouped_fwd(const uint8_t *packed, const uint8_t *q, const float *s
   std::memset(&a, 0, sizeof a);
   const uint32_t box = static_cast<uint32_t>(128 * p.ntt);
   if (!map_tokens_3d(&a.tm_b, X, s.T, s.K, box, 1) ||
-      !make_map(&a.tm_pk, packed, MAP_U8, s.K / 2, s.E * s.N, s.K / 2, 128, 128, SW_128B) ||
+      !map_codes_fwd(&a.tm_pk, packed, s.E * s.N, s.K, p.ntt == 2 ? GroupedFwd2::KSUP : GroupedFwd1::KSUP) ||
       !map_experts_3d(&a.tm_a2, B, s.N, s.r, s.E, 64, 64) || !map_kmajor(&a.tm_b2, xas, s.r, s.T, box))
     return QLORA_ERR_CUDA;
   grouped_gemm_args(&a, q, scale2, nf4, t8, s, g, s.N, s.K / 64, Y, part, counters);
@@ -383,7 +383,7 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
   std::memset(&a, 0, sizeof a);
   const uint32_t box = static_cast<uint32_t>(128 * p.ntt);
   if (!map_tokens_3d(&a.tm_b, dY, s.T, s.N, box, 1) ||
-      !make_map(&a.tm_pk, packed, MAP_U8, s.K / 2, s.E * s.N, s.K / 2, 64, 256, SW_64B) ||
+      !map_codes_bwd(&a.tm_pk, packed, s.E * s.N, s.K, p.ntt == 2 ? GroupedBwd2::KSUP : GroupedBwd1::KSUP) ||
       !map_experts_3d(&a.tm_a2, A, s.r, s.K, s.E, 64, 128) || !map_kmajor(&a.tm_b2, gs, s.r, s.T, box))
     return QLORA_ERR_CUDA;
   grouped_gemm_args(&a, q, scale2, nf4, t8, s, g, s.K, s.N / 64, dX, part, counters);

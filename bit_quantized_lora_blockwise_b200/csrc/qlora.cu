@@ -313,6 +313,15 @@ bool map_mnmajor(CUtensorMap *m, const void *p, int64_t inner, int64_t outer) {
   return make_map(m, p, MAP_BF16, inner, outer, inner * 2, 64, 64, SW_128B);
 }
 
+// Packed codes [N, K/2] as the fused GEMM's slots of ksup K blocks take them:
+// 32 ksup bytes of 128 rows (forward), 64 bytes of 64 ksup rows (backward).
+bool map_codes_fwd(CUtensorMap *m, const void *packed, int64_t N, int64_t K, int ksup) {
+  return make_map(m, packed, MAP_U8, K / 2, N, K / 2, 32 * ksup, 128, ksup == 4 ? SW_128B : SW_64B);
+}
+bool map_codes_bwd(CUtensorMap *m, const void *packed, int64_t N, int64_t K, int ksup) {
+  return make_map(m, packed, MAP_U8, K / 2, N, K / 2, 64, 64 * ksup, SW_64B);
+}
+
 // Token operand T [tokens, kdim] bf16 viewed as {64, tokens, kdim/64} (k
 // within a 64-block, token, block): box {64, box_rows, bkb} lands as bkb
 // consecutive K-major 128-byte-swizzled [box_rows][64] tiles.
@@ -658,7 +667,7 @@ qlora_status skinny(SkinnyKind kind, const void *aop, int64_t a_inner, int64_t a
 // cluster of two CTAs): six token stages of one K block of 128 tokens (one
 // 16 KB TMA box each), dequantized-weight stages of one K block (16 KB) and
 // packed-code slots of 4 K blocks (18 KB).
-constexpr int kPairBkb = 1, kPairSb = 4, kPairSa = 5, kPairSp = 3, kPairNpw = 16;
+constexpr int kPairBkb = 1, kPairSb = 5, kPairSa = 5, kPairSp = 3, kPairNpw = 16;
 using FwdPairCfg = GemmCfg<256, A_DEQ_K, L2_A_MN, kPairBkb, kPairSb, kPairSa, kPairSp, kPairNpw, true>;
 using BwdPairCfg = GemmCfg<256, A_DEQ_MN, L2_A_K, kPairBkb, kPairSb, kPairSa, kPairSp, kPairNpw, true>;
 // Two 256-token sub-tiles per job (512 tokens per tile, each CTA loading 256
@@ -666,7 +675,7 @@ using BwdPairCfg = GemmCfg<256, A_DEQ_MN, L2_A_K, kPairBkb, kPairSb, kPairSa, kP
 // two of two blocks hide a refill behind three stages of MMAs, 2-3 % faster
 // on the 7B shapes), 3 dequantized-weight stages, 2 packed-code slots (212 KB
 // of shared memory).
-constexpr int kPair2Bkb = 1, kPair2Sb = 3, kPair2Sa = 5, kPair2Sp = 2, kPair2Npw = 12;
+constexpr int kPair2Bkb = 1, kPair2Sb = 4, kPair2Sa = 4, kPair2Sp = 2, kPair2Npw = 12;
 using FwdPair2Cfg = GemmCfg<256, A_DEQ_K, L2_A_MN, kPair2Bkb, kPair2Sb, kPair2Sa, kPair2Sp, kPair2Npw, true, 2>;
 using BwdPair2Cfg = GemmCfg<256, A_DEQ_MN, L2_A_K, kPair2Bkb, kPair2Sb, kPair2Sa, kPair2Sp, kPair2Npw, true, 2>;
 // token counts from which a tile holds two 256-token sub-tiles
@@ -1135,7 +1144,7 @@ qlora_status qlora_linear_fwd(const uint8_t *packed, const uint8_t *q, const flo
   GemmArgs a;
   std::memset(&a, 0, sizeof a);
   if (!map_tokens_3d(&a.tm_b, X, M, K, b_rows, bkb) ||
-      !make_map(&a.tm_pk, packed, MAP_U8, K / 2, N, K / 2, 128, 128, SW_128B) ||
+      !map_codes_fwd(&a.tm_pk, packed, N, K, fp.pair && fp.ntt == 2 ? FwdPair2Cfg::KSUP : FwdPairCfg::KSUP) ||
       !map_mnmajor(&a.tm_a2, B, N, r) || !map_kmajor(&a.tm_b2, xas, r, M, b_rows))
     return QLORA_ERR_CUDA;
   a.rows = static_cast<int>(N);
@@ -1214,7 +1223,7 @@ qlora_status qlora_linear_bwd(const uint8_t *packed, const uint8_t *q, const flo
   GemmArgs a;
   std::memset(&a, 0, sizeof a);
   if (!map_tokens_3d(&a.tm_b, dY, M, N, b_rows, bkb) ||
-      !make_map(&a.tm_pk, packed, MAP_U8, K / 2, N, K / 2, 64, 256, SW_64B) ||
+      !map_codes_bwd(&a.tm_pk, packed, N, K, fp.pair && fp.ntt == 2 ? BwdPair2Cfg::KSUP : BwdPairCfg::KSUP) ||
       !map_kmajor(&a.tm_a2, A, r, K, 128) || !map_kmajor(&a.tm_b2, gs, r, M, b_rows))
     return QLORA_ERR_CUDA;
   a.rows = static_cast<int>(K);
