@@ -63,16 +63,29 @@ __device__ __forceinline__ uint32_t dropout_keep8(const DropoutArgs &d, uint64_t
   return keep;
 }
 
+// The same as masks of the four words of eight 16-bit elements.
+__device__ __forceinline__ uint4 dropout_mask8(const DropoutArgs &d, uint64_t group) {
+  const uint4 w = philox4x32_10(d.seed, d.offset + group);
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  uint32_t m[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    bool lo, hi;
+    keep_pair(u[j], d.threshold, lo, hi);
+    m[j] = (lo ? 0x0000FFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
+  }
+  return make_uint4(m[0], m[1], m[2], m[3]);
+}
+
 enum DropoutType : int { DROP_BF16 = 0, DROP_F16 = 1, DROP_F32 = 2 };
 
 // Two elements of a word's halves: kept ones times the factor (fp32 product,
 // one rounding), the others +0, whatever they held (a dropped NaN or infinity
-// is 0). SCALE = false: the factor is 1.
-template <int TYPE, bool SCALE>
+// is 0).
+template <int TYPE>
 __device__ __forceinline__ uint32_t dropout_pair(uint32_t v, bool klo, bool khi, float factor) {
   v = klo ? v : v & 0xFFFF0000u;
   v = khi ? v : v & 0x0000FFFFu;
-  if constexpr (!SCALE) return v;
   float lo, hi;
   if constexpr (TYPE == DROP_F16) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v));
@@ -86,7 +99,7 @@ __device__ __forceinline__ uint32_t dropout_pair(uint32_t v, bool klo, bool khi,
 }
 
 // The same for the eight elements of one counter.
-template <int TYPE, bool SCALE>
+template <int TYPE>
 __device__ __forceinline__ uint4 dropout_eight(const uint4 &v, const DropoutArgs &d, uint64_t group, float factor) {
   const uint4 w = philox4x32_10(d.seed, d.offset + group);
   const uint32_t u[4] = {w.x, w.y, w.z, w.w}, x[4] = {v.x, v.y, v.z, v.w};
@@ -95,7 +108,7 @@ __device__ __forceinline__ uint4 dropout_eight(const uint4 &v, const DropoutArgs
   for (int j = 0; j < 4; ++j) {
     bool lo, hi;
     keep_pair(u[j], d.threshold, lo, hi);
-    y[j] = dropout_pair<TYPE, SCALE>(x[j], lo, hi, factor);
+    y[j] = dropout_pair<TYPE>(x[j], lo, hi, factor);
   }
   return make_uint4(y[0], y[1], y[2], y[3]);
 }
@@ -103,9 +116,9 @@ __device__ __forceinline__ uint4 dropout_eight(const uint4 &v, const DropoutArgs
 // y[i] = keep(i) ? x[i] * factor : 0 over n elements; x and y 16-byte
 // aligned, y == x allowed. One thread per counter (8 elements: one 16-byte
 // load and store for 16-bit types, two for fp32).
-template <int TYPE, bool SCALE = true>
-__global__ void __launch_bounds__(256) dropout_kernel(const void *x, void *y, int64_t n, const DropoutArgs d,
-                                                      float factor) {
+template <int TYPE>
+__global__ void __launch_bounds__(256) dropout_kernel(const void *x, void *y, int64_t n, const DropoutArgs d) {
+  const float factor = d.factor;
   grid_dep_wait();
   grid_dep_launch();
   const int64_t full = n / 8;
@@ -123,7 +136,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const void *x, void *y, in
                       k & 128u ? b.w * factor : 0.0f);
     } else {
       const uint4 v = reinterpret_cast<const uint4 *>(x)[g];
-      reinterpret_cast<uint4 *>(y)[g] = dropout_eight<TYPE, SCALE>(v, d, static_cast<uint64_t>(g), factor);
+      reinterpret_cast<uint4 *>(y)[g] = dropout_eight<TYPE>(v, d, static_cast<uint64_t>(g), factor);
     }
   }
   // the last, partial counter: one thread, element by element
@@ -137,7 +150,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const void *x, void *y, in
         reinterpret_cast<float *>(y)[i] = (k >> j) & 1u ? v * factor : 0.0f;
       } else {
         const uint32_t v = reinterpret_cast<const uint16_t *>(x)[i];
-        reinterpret_cast<uint16_t *>(y)[i] = static_cast<uint16_t>(dropout_pair<TYPE, SCALE>(v, (k >> j) & 1u, true, factor));
+        reinterpret_cast<uint16_t *>(y)[i] = static_cast<uint16_t>(dropout_pair<TYPE>(v, (k >> j) & 1u, true, factor));
       }
     }
   }

@@ -87,17 +87,16 @@ GroupedBwdPlan plan_grouped_bwd(const GroupedShape &s, int sms) {
   return p;
 }
 
-// [counters][16-bit T x r][16-bit T x r (backward)][16-bit T x K: M o X, with dropout][fp32 partials]
+// [counters][16-bit T x r][16-bit T x r (backward)][fp32 partials]
 struct GroupedWs {
-  size_t counters, tr, xm, part, total;
+  size_t counters, tr, part, total;
 };
 GroupedWs grouped_ws(const GroupedShape &s, int64_t ncounters, size_t part, bool backward) {
   GroupedWs w;
   w.counters = align256(static_cast<size_t>(ncounters) * 4);
   w.tr = align256(static_cast<size_t>(s.T) * s.r * 2);
-  w.xm = s.drop ? align256(static_cast<size_t>(s.T) * s.K * 2) : 0;
   w.part = part;
-  w.total = w.counters + (backward ? 2 : 1) * w.tr + w.xm + w.part;
+  w.total = w.counters + (backward ? 2 : 1) * w.tr + w.part;
   return w;
 }
 
@@ -129,15 +128,11 @@ qlora_status make_dropout(const qlora_dropout_desc *d, DropoutArgs *out) {
 }
 
 // One thread per 8 elements, at most eight CTAs per SM in one wave.
-qlora_status run_dropout(const void *x, void *y, int64_t n, int type, const DropoutArgs &d, float factor, int sms,
-                         cudaStream_t st) {
+qlora_status run_dropout(const void *x, void *y, int64_t n, int type, const DropoutArgs &d, int sms, cudaStream_t st) {
   const int grid = grid_for(cdiv(n, 8), 256, sms, 8);
-  // the adapter branch's M o X: kept 16-bit elements as they are
-  if (factor == 1.0f && type != DROP_F32)
-    return launch_pdl(dropout_kernel<DROP_BF16, false>, grid, 256, 0, st, x, y, n, d, factor);
-  if (type == DROP_F32) return launch_pdl(dropout_kernel<DROP_F32>, grid, 256, 0, st, x, y, n, d, factor);
-  if (type == DROP_F16) return launch_pdl(dropout_kernel<DROP_F16>, grid, 256, 0, st, x, y, n, d, factor);
-  return launch_pdl(dropout_kernel<DROP_BF16>, grid, 256, 0, st, x, y, n, d, factor);
+  if (type == DROP_F32) return launch_pdl(dropout_kernel<DROP_F32>, grid, 256, 0, st, x, y, n, d);
+  if (type == DROP_F16) return launch_pdl(dropout_kernel<DROP_F16>, grid, 256, 0, st, x, y, n, d);
+  return launch_pdl(dropout_kernel<DROP_BF16>, grid, 256, 0, st, x, y, n, d);
 }
 
 // Expert stack of 16-bit matrices [groups][outer][inner]: box {box_inner, box_outer, 1}.
@@ -156,16 +151,18 @@ bool map_experts_3d(CUtensorMap *map, const void *p, int64_t inner, int64_t oute
   return r == CUDA_SUCCESS;
 }
 
-// out[T, r] = scale * rows . adapter_e: X A (kind SK_XA) or dY B^T (SK_G),
-// optionally a second copy with another scale.
+// out[T, r] = scale * rows . adapter_e: X A (kind SK_XA; with dropout (M o X)
+// A) or dY B^T (SK_G), optionally a second copy with another scale.
 qlora_status grouped_rows(SkinnyKind kind, const void *rows, const void *adapter, const GroupedShape &s,
-                          const GroupArgs &g, void *out, float scale, void *out2, float scale2,
+                          const GroupArgs &g, const DropoutArgs &drop, void *out, float scale, void *out2, float scale2,
                           unsigned int *zero_words, int64_t nzero, cudaStream_t st) {
   const int64_t kdim = kind == SK_XA ? s.K : s.N;
   const int64_t tiles = token_tiles_bound(s.T, s.E, 128);
+  const bool masked = kind == SK_XA && s.drop;
   SkinnyPlan p;
-  qlora_status e = kind == SK_XA ? plan_skinny_v<false, true, true>(tiles * 128, kdim, s.r, &p)
-                                 : plan_skinny_v<false, false, true>(tiles * 128, kdim, s.r, &p);
+  qlora_status e = masked          ? plan_skinny_v<false, true, true, true>(tiles * 128, kdim, s.r, &p)
+                   : kind == SK_XA ? plan_skinny_v<false, true, true>(tiles * 128, kdim, s.r, &p)
+                                   : plan_skinny_v<false, false, true>(tiles * 128, kdim, s.r, &p);
   if (e != QLORA_OK) return e;
   SkinnyArgs a;
   std::memset(&a, 0, sizeof a);
@@ -190,27 +187,32 @@ qlora_status grouped_rows(SkinnyKind kind, const void *rows, const void *adapter
   a.nzero = static_cast<int>(nzero);
   a.f16 = t_f16 ? 1 : 0;
   a.groups = g;
+  P.masked = masked ? 1 : 0;
+  a.drop = drop;
+  a.drop_ld = s.K;
+  if (masked) return run_skinny<false, true, true, true>(a, p.bn, grid, st);
   return kind == SK_XA ? run_skinny<false, true, true>(a, p.bn, grid, st)
                        : run_skinny<false, false, true>(a, p.bn, grid, st);
 }
 
-// dA_e = xm_e^T gs_e and dB_e = s xa_e^T dY_e, every expert's in one launch.
-qlora_status grouped_adapter_grads(const void *xm, const void *dY, const void *gs, const void *xa, const GroupedShape &s,
-                                   const GroupArgs &g, void *dA, float a_scale, void *dB, float b_scale,
+// dA_e = (M o X_e)^T gs_e and dB_e = s xa_e^T dY_e, every expert's in one launch.
+qlora_status grouped_adapter_grads(const void *X, const void *dY, const void *gs, const void *xa, const GroupedShape &s,
+                                   const GroupArgs &g, const DropoutArgs &drop, void *dA, void *dB, float b_scale,
                                    cudaStream_t st) {
   const int64_t ta = s.E * cdiv(s.K, 128), tb = s.E * cdiv(s.N, 128);
   SkinnyPlan p;
-  const qlora_status e = plan_skinny_v<true, true, true>((ta + tb) * 128, cdiv(s.T, s.E), s.r, &p);
+  const qlora_status e = s.drop ? plan_skinny_v<true, true, true, true>((ta + tb) * 128, cdiv(s.T, s.E), s.r, &p)
+                                : plan_skinny_v<true, true, true>((ta + tb) * 128, cdiv(s.T, s.E), s.r, &p);
   if (e != QLORA_OK) return e;
   SkinnyArgs a;
   std::memset(&a, 0, sizeof a);
   SkinnyProblem &A = a.prob[0], &B = a.prob[1];
-  if (!map_mnmajor(&A.tm_a, xm, s.K, s.T) || !map_mnmajor(&A.tm_b, gs, s.r, s.T) ||
+  if (!map_mnmajor(&A.tm_a, X, s.K, s.T) || !map_mnmajor(&A.tm_b, gs, s.r, s.T) ||
       !map_mnmajor(&B.tm_a, dY, s.N, s.T) || !map_mnmajor(&B.tm_b, xa, s.r, s.T))
     return QLORA_ERR_CUDA;
   A.out = dA;
   A.out_ld = s.r;
-  A.out_scale = a_scale;
+  A.out_scale = 1.0f;
   A.rows = static_cast<int>(s.K);
   A.cols = s.r;
   B.out = dB;
@@ -224,7 +226,12 @@ qlora_status grouped_adapter_grads(const void *xm, const void *dY, const void *g
   a.late = 1;
   a.f16 = t_f16 ? 1 : 0;
   a.groups = g;
-  return run_skinny<true, true, true>(a, p.bn, static_cast<int>(ta + tb) * p.splits, st);
+  const int grid = static_cast<int>(ta + tb) * p.splits;
+  if (!s.drop) return run_skinny<true, true, true>(a, p.bn, grid, st);
+  A.masked = 1;
+  a.drop = drop;
+  a.drop_ld = s.K;
+  return run_skinny<true, true, true, true>(a, p.bn, grid, st);
 }
 
 template <class C>
@@ -281,25 +288,17 @@ qlora_status grouped_fwd(const uint8_t *packed, const uint8_t *q, const float *s
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   unsigned int *counters = reinterpret_cast<unsigned int *>(ws);
   void *xas = ws + w.counters;
-  void *xm = ws + w.counters + w.tr;
-  float *part = reinterpret_cast<float *>(ws + w.counters + w.tr + w.xm);
+  float *part = reinterpret_cast<float *>(ws + w.counters + w.tr);
   const GroupArgs g{offsets, static_cast<int>(s.E), static_cast<int>(s.T)};
   const float scl = alpha / static_cast<float>(s.r);
   qlora_status st = QLORA_OK;
 
-  // 1) the adapter branch's input: M o X (kept elements as they are: exact;
-  //    the factor 1 / (1 - p) goes into the fp32 scales below)
-  const void *xin = X;
-  if (s.drop) {
-    st = run_dropout(X, xm, s.T * s.K, t_f16 ? DROP_F16 : DROP_BF16, drop, 1.0f, sms, cs);
-    if (st != QLORA_OK) return st;
-    xin = xm;
-  }
-  // 2) XA, and s XA for the low-rank step; zeroes the counters
-  st = grouped_rows(SK_XA, xin, A, s, g, xas, scl * drop.factor, XA_out, drop.factor, counters, p.counters, cs);
+  // 1) XA = D(X) A, and s XA for the low-rank step (the dropout factor in
+  //    both scales: the product itself reads M o X); zeroes the counters
+  st = grouped_rows(SK_XA, X, A, s, g, drop, xas, scl * drop.factor, XA_out, drop.factor, counters, p.counters, cs);
   if (st != QLORA_OK) return st;
 
-  // 3) the base product, whose main loop overlaps 2)
+  // 2) the base product, whose main loop overlaps 1)
   if (p.stream) {
     SmallmArgs a;
     std::memset(&a, 0, sizeof a);
@@ -355,27 +354,20 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
   unsigned int *counters = reinterpret_cast<unsigned int *>(ws);
   void *gs = ws + w.counters;
   void *xa_ws = ws + w.counters + w.tr;
-  void *xm = ws + w.counters + 2 * w.tr;
-  float *part = reinterpret_cast<float *>(ws + w.counters + 2 * w.tr + w.xm);
+  float *part = reinterpret_cast<float *>(ws + w.counters + 2 * w.tr);
   const GroupArgs g{offsets, static_cast<int>(s.E), static_cast<int>(s.T)};
   const float scl = alpha / static_cast<float>(s.r);
   qlora_status st = QLORA_OK;
 
-  // 1) M o X again (never kept from the forward), XA where it was not saved,
-  //    and Gs = s dY B^T times the dropout factor (dX and dA mask it, nothing
-  //    else), whose launch zeroes the counters
-  const void *xin = X;
-  if (s.drop) {
-    st = run_dropout(X, xm, s.T * s.K, t_f16 ? DROP_F16 : DROP_BF16, drop, 1.0f, sms, cs);
-    if (st != QLORA_OK) return st;
-    xin = xm;
-  }
+  // 1) XA where it was not saved, and Gs = s dY B^T times the dropout factor
+  //    (dX and dA mask it, nothing else reads it), whose launch zeroes the
+  //    counters
   if (XA == nullptr) {
-    st = grouped_rows(SK_XA, xin, A, s, g, xa_ws, drop.factor, nullptr, 0.0f, nullptr, 0, cs);
+    st = grouped_rows(SK_XA, X, A, s, g, drop, xa_ws, drop.factor, nullptr, 0.0f, nullptr, 0, cs);
     if (st != QLORA_OK) return st;
     XA = xa_ws;
   }
-  st = grouped_rows(SK_G, dY, B, s, g, gs, scl * drop.factor, nullptr, 0.0f, counters, p.counters, cs);
+  st = grouped_rows(SK_G, dY, B, s, g, drop, gs, scl * drop.factor, nullptr, 0.0f, counters, p.counters, cs);
   if (st != QLORA_OK) return st;
 
   // 2) dX
@@ -398,5 +390,5 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
 
   // 3) dA and dB "late", as in the dense backward: every operand is complete
   //    when this launch starts and dX is neither read nor written by it
-  return grouped_adapter_grads(xin, dY, gs, XA, s, g, dA, 1.0f, dB, scl, cs);
+  return grouped_adapter_grads(X, dY, gs, XA, s, g, drop, dA, dB, scl, cs);
 }

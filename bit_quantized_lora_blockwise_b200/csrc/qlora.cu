@@ -459,9 +459,9 @@ constexpr int skinny_stages(int bn) { return bn == 64 ? 4 : (bn == 128 ? 3 : 4);
 // One skinny-GEMM variant: its shared-memory opt-in and how many clusters
 // of 2, 4 and 8 CTAs can be resident at once (asked of the runtime once per
 // device).
-template <int BN, bool AMN, bool BMN, bool GROUPED = false>
+template <int BN, bool AMN, bool BMN, bool GROUPED = false, bool DROP = false>
 struct SkinnyVariant {
-  using C = SkinnyCfg<BN, AMN, BMN, skinny_stages(BN), GROUPED>;
+  using C = SkinnyCfg<BN, AMN, BMN, skinny_stages(BN), GROUPED, DROP>;
   static qlora_status prepare(int (&max_clusters)[4], int *per_sm) {
     static std::once_flag once[kMaxDevices];
     static cudaError_t err[kMaxDevices];
@@ -519,15 +519,15 @@ struct SkinnyPlan {
 // Split K over a cluster of 2, 4 or 8 CTAs per 128-row tile: the largest
 // split whose clusters for all row tiles are resident at once (one wave),
 // else one CTA per tile.
-template <bool AMN, bool BMN, bool GROUPED = false>
+template <bool AMN, bool BMN, bool GROUPED = false, bool DROP = false>
 qlora_status plan_skinny_v(int64_t rows, int64_t kdim, int r, SkinnyPlan *p) {
   p->rows = static_cast<int>(rows);
   p->kblocks = static_cast<int>(cdiv(kdim, 64));
   p->bn = rank_tile(r);
   int maxc[4];
-  const qlora_status st = p->bn == 64    ? SkinnyVariant<64, AMN, BMN, GROUPED>::prepare(maxc, &p->per_sm)
-                          : p->bn == 128 ? SkinnyVariant<128, AMN, BMN, GROUPED>::prepare(maxc, &p->per_sm)
-                                         : SkinnyVariant<256, AMN, BMN, GROUPED>::prepare(maxc, &p->per_sm);
+  const qlora_status st = p->bn == 64    ? SkinnyVariant<64, AMN, BMN, GROUPED, DROP>::prepare(maxc, &p->per_sm)
+                          : p->bn == 128 ? SkinnyVariant<128, AMN, BMN, GROUPED, DROP>::prepare(maxc, &p->per_sm)
+                                         : SkinnyVariant<256, AMN, BMN, GROUPED, DROP>::prepare(maxc, &p->per_sm);
   const int row_tiles = static_cast<int>(cdiv(rows, 128));
   p->splits = 1;
   for (int l = 3; l >= 1; --l)
@@ -538,9 +538,9 @@ qlora_status plan_skinny_v(int64_t rows, int64_t kdim, int r, SkinnyPlan *p) {
   return st;
 }
 
-template <int BN, bool AMN, bool BMN, bool GROUPED = false>
+template <int BN, bool AMN, bool BMN, bool GROUPED = false, bool DROP = false>
 qlora_status run_skinny_bn(const SkinnyArgs &a, int grid, cudaStream_t st) {
-  using C = typename SkinnyVariant<BN, AMN, BMN, GROUPED>::C;
+  using C = typename SkinnyVariant<BN, AMN, BMN, GROUPED, DROP>::C;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(C::THREADS);
@@ -560,11 +560,11 @@ qlora_status run_skinny_bn(const SkinnyArgs &a, int grid, cudaStream_t st) {
   return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
-template <bool AMN, bool BMN, bool GROUPED = false>
+template <bool AMN, bool BMN, bool GROUPED = false, bool DROP = false>
 qlora_status run_skinny(const SkinnyArgs &a, int bn, int grid, cudaStream_t st) {
-  if (bn == 64) return run_skinny_bn<64, AMN, BMN, GROUPED>(a, grid, st);
-  if (bn == 128) return run_skinny_bn<128, AMN, BMN, GROUPED>(a, grid, st);
-  return run_skinny_bn<256, AMN, BMN, GROUPED>(a, grid, st);
+  if (bn == 64) return run_skinny_bn<64, AMN, BMN, GROUPED, DROP>(a, grid, st);
+  if (bn == 128) return run_skinny_bn<128, AMN, BMN, GROUPED, DROP>(a, grid, st);
+  return run_skinny_bn<256, AMN, BMN, GROUPED, DROP>(a, grid, st);
 }
 
 
@@ -1739,7 +1739,7 @@ qlora_status qlora_dropout(const void *x, void *y, int64_t n, qlora_element type
   DeviceInfo dev;
   if ((st = device_info(&dev)) != QLORA_OK) return st;
   if (n == 0) return QLORA_OK;
-  return run_dropout(x, y, n, static_cast<int>(type), d, d.factor, dev.sms, static_cast<cudaStream_t>(stream));
+  return run_dropout(x, y, n, static_cast<int>(type), d, dev.sms, static_cast<cudaStream_t>(stream));
 }
 
 size_t qlora_grouped_workspace_bytes(int E, int64_t T, int64_t N, int64_t K, int r, int dropout) {

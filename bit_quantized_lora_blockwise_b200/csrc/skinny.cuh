@@ -27,9 +27,19 @@
 // rows of both operands to zero in shared memory before the MMAs read them,
 // so that not even a NaN there can enter this expert's gradient. An expert
 // without tokens gets zeros.
+//
+// Adapter dropout (DROP = true): the product reads M o X in place of X (kept
+// elements as they are; the factor is in the output's scale). X never makes
+// a pass of its own: warps 4-7, idle until the readout, take each landed
+// 16 KB stage of X through the mask in shared memory before the MMAs read
+// it, 16 bytes (8 elements, one Philox counter) at a time. Bound by that
+// integer work, about 1000 clocks a stage and SM, 4.5 TB/s of X. (A dropout
+// launch ahead of the product wrote and re-read X: 840 us against 777 for the
+// whole backward of 8192 rows through 4096 x 11008.)
 #pragma once
 
 #include "codec.cuh"
+#include "dropout.cuh"
 #include "groups.cuh"
 #include "ptx.cuh"
 
@@ -47,6 +57,7 @@ struct SkinnyProblem {
   int rows;     // extent of the 128-row MMA dimension
   int cols;     // r
   int kblocks;  // 64-deep K blocks in total
+  int masked;   // DROP: the A operand is taken through the mask (X; not dY)
 };
 
 struct SkinnyArgs {
@@ -64,11 +75,14 @@ struct SkinnyArgs {
               // thread waits for it only before exiting, so this grid still completes after it
   int f16;   // operands and outputs are fp16 (else bf16)
   GroupArgs groups;  // GROUPED only; prob[i].rows is then per expert for products over the tokens
+  DropoutArgs drop;  // DROP only
+  int64_t drop_ld;   // row length of the masked operand X
 };
 
-template <int BN_, bool A_MN_, bool B_MN_, int STAGES_, bool GROUPED_ = false>
+template <int BN_, bool A_MN_, bool B_MN_, int STAGES_, bool GROUPED_ = false, bool DROP_ = false>
 struct SkinnyCfg {
-  static constexpr bool GROUPED = GROUPED_;
+  static constexpr bool GROUPED = GROUPED_, DROP = DROP_;
+  static_assert(!DROP_ || GROUPED_, "dropout comes with groups");
   static constexpr int BN = BN_, STAGES = STAGES_;
   static constexpr bool A_MN = A_MN_, B_MN = B_MN_;
   static_assert(BN_ % 64 == 0 && BN_ <= 256, "rank tile");
@@ -77,8 +91,9 @@ struct SkinnyCfg {
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = STAGES_ * A_BYTES;
   static constexpr int OFF_BAR = OFF_B + STAGES_ * B_BYTES;
-  static constexpr int NBARS = 2 * STAGES_ + (GROUPED_ ? 4 : 2);  // full[S], empty[S], tmem_full, drain, (landed, tail)
-  static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
+  // full[S], empty[S], tmem_full, drain, (GROUPED: landed, tail), (DROP: ready[S])
+  static constexpr int NBARS = 2 * STAGES_ + (GROUPED_ ? 4 : 2) + (DROP_ ? STAGES_ : 0);
+  static constexpr int OFF_MISC = (OFF_BAR + NBARS * 8 + 15) & ~15;
   static constexpr int OFF_GROUPS = OFF_MISC + 16;
   static constexpr int SMEM_BYTES = OFF_GROUPS + (GROUPED_ ? kGroupTableBytes : 0);
   static constexpr int THREADS = 256;
@@ -111,6 +126,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
   const uint32_t rank = splits > 1 ? cluster_ctarank() : 0u;
   const int tile = local_block / splits;
   const uint32_t landed_bar = bar0 + 8u * (2 * C::STAGES + 2), tail_bar = landed_bar + 8u;
+  auto ready_bar = [&](int s) { return bar0 + 8u * (2 * C::STAGES + 4 + s); };
   int row0 = tile * 128;
   int row_end = P.rows;    // one past the tile's last row
   int kblocks = P.kblocks;
@@ -156,6 +172,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
       mbar_init(landed_bar, 1);
       mbar_init(tail_bar, 1);
     }
+    for (int s = 0; s < C::STAGES && C::DROP; ++s) mbar_init(ready_bar(s), 4);
     *s_abort = 0;
     fence_barrier_init();
   }
@@ -243,7 +260,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
       bool ok = true;
       for (int j = 0; j < nk; ++j) {
         const int s = j % C::STAGES;
-        if (!mbar_wait(full_bar(s), (j / C::STAGES) & 1u, s_abort)) { ok = false; break; }
+        const uint32_t landed = C::DROP && P.masked ? ready_bar(s) : full_bar(s);
+        if (!mbar_wait(landed, (j / C::STAGES) & 1u, s_abort)) { ok = false; break; }
         if (C::GROUPED && tail_rows > 0 && j == nk - 1) {
           mbar_arrive(landed_bar);  // (only this thread follows the ring's phases)
           if (!mbar_wait(tail_bar, 0, s_abort)) { ok = false; break; }
@@ -290,8 +308,39 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
       }
     }
   } else if (warp >= 4) {
-    // TMEM -> this CTA's fp32 partial in shared memory (the ring is idle now)
     const int q = warp - 4;
+    if constexpr (C::DROP) {
+      // M o X, stage by stage. 16-byte piece c of row r of a 64-wide K-major
+      // (or MN-major) chunk lies at c ^ (r & 7) in the row's 128 bytes. A
+      // thread's eight pieces are 16 rows apart; their masks are formed side
+      // by side before the stage is waited for. Rows of no token of this
+      // expert are masked too: never stored (K-major) or zeroed by warp 2.
+      const int tid = q * 32 + lane, c = tid & 7, r0 = tid >> 3;
+      const uint32_t swz = static_cast<uint32_t>(c ^ (r0 & 7)) << 4;  // (the same for rows 16 apart)
+      const uint64_t ld8 = static_cast<uint64_t>(args.drop_ld) / 8;
+      for (int j = 0; P.masked && j < nk; ++j) {
+        const int s = j % C::STAGES, kb = kb_begin + j;
+        // counter of the piece in row r0: K-major 128 token rows of one chunk, MN-major 64 token rows of two
+        const uint64_t first = C::A_MN ? static_cast<uint64_t>(tok0 + kb * 64 + r0) * ld8 + (row0 / 8 + c)
+                                       : static_cast<uint64_t>(row0 + r0) * ld8 + (kb * 8 + c);
+        uint4 mask[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          mask[i] = dropout_mask8(args.drop, first + (C::A_MN ? (i & 3) * 16 * ld8 + (i >> 2) * 8 : i * 16 * ld8));
+        if (!warp_wait_all(full_bar(s), (j / C::STAGES) & 1u, s_abort)) break;
+        uint8_t *piece = smem + C::OFF_A + s * C::A_BYTES + r0 * 128 + swz;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint4 *at = reinterpret_cast<uint4 *>(piece + i * 2048);
+          const uint4 v = *at;
+          *at = make_uint4(v.x & mask[i].x, v.y & mask[i].y, v.z & mask[i].z, v.w & mask[i].w);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ready_bar(s));
+      }
+    }
+    // TMEM -> this CTA's fp32 partial in shared memory (the ring is idle now)
     const bool ok = (!C::GROUPED || nk > 0) && warp_wait_all(tmem_full, 0, s_abort);
     tc_fence_after();
     float *part = reinterpret_cast<float *>(smem);
