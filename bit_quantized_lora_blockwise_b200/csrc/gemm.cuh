@@ -151,8 +151,9 @@ struct GemmCfg {
   // One ring for both operands: a job's tokens and decoded weights share a
   // stage, one full barrier and one release. The MMA thread's work per job
   // (its instructions are fetched anew each time, beside the dequant warps'
-  // long loop) sets the pace of the 256-token tiles: two rings cost it two
-  // waits and two commits, 850 clocks a job against 790.
+  // long loop) paces the 256-token tiles: two rings cost it two waits and two
+  // commits, 850 clocks a job against 790. (Two jobs per stage as well: 700,
+  // but the code slots that their room costs starve the dequant warps.)
   static constexpr bool ONE_RING = BKB_ == 1 && SA_ == SB_;
   static_assert(NPW_ % 4 == 0 && NPW_ >= 4 && SP_ >= 2, "producer groups of 4 warps and a packed-code ring");
   // (a 16-warp, 3-slot configuration timed out on B200: every producer group

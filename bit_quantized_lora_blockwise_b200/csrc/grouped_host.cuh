@@ -4,8 +4,8 @@
 //
 // The host knows E and T but not the offsets, so it sizes grids and
 // workspaces for the worst split of T tokens over E experts, and picks
-// variants from the average tokens per expert; every variant is right for
-// every split.
+// the tile from the average tokens per expert; either is right for every
+// split.
 
 // An expert of c tokens has ceil(c / tile) token tiles: at most T / tile full
 // ones in all and one partial one per expert with tokens.
@@ -19,9 +19,15 @@ struct GroupedShape {
   bool drop;
 };
 
-// Variant choice by the average tokens per expert (T / E).
-constexpr int64_t kGroupedStreamTokens = 24;   // up to here: the register-dequant stream
-constexpr int64_t kGroupedTwoSubtile = 384;    // from here: two 256-token sub-tiles per tile
+// Two 256-token sub-tiles per tile from this average of tokens per expert
+// (T / E) on; one below it. (8 experts, 4096 columns: at 256 tokens an expert
+// 11008 rows take 200 us with one and 214 with two, at 375 276 and 262. The
+// same 256-token tiles serve a single token: the dequantization, not the
+// tokens, sets their time. A stream over the codes with register decode, as
+// the dense call's few-token path, took 131 us against 126 for 32 rows over 8
+// experts and lost from 5 rows an expert on; 128-token tiles with a deeper
+// ring were within 1 %.)
+constexpr int64_t kGroupedTwoSubtile = 320;
 
 using GroupedFwd1 = GemmCfg<256, A_DEQ_K, L2_A_MN, kPairBkb, kPairSb, kPairSa, kPairSp, kPairNpw, true, 1, true>;
 using GroupedFwd2 = GemmCfg<256, A_DEQ_K, L2_A_MN, kPair2Bkb, kPair2Sb, kPair2Sa, kPair2Sp, kPair2Npw, true, 2, true>;
@@ -39,51 +45,23 @@ int grouped_pair_slots(int sms) {
   return std::min(n, sms / 2);  // 0 without a device: the calls then return before any launch
 }
 
-struct GroupedFwdPlan {
-  bool stream;
-  int nt, kc, grid;  // stream: 8 nt tokens per pass
-  int64_t bands, counters;
-  int ntt, slots;    // GEMM
-  size_t part;
-};
-
 // Partials of a grouped GEMM split over K: splits x tiles <= slots (plan_grouped).
 size_t grouped_part_bytes(int slots, int ntt, int64_t kblocks) {
   return kblocks / 4 >= 2 ? align256(static_cast<size_t>(slots) * 256 * ntt * 256 * 4) : 0;
 }
 
-GroupedFwdPlan plan_grouped_fwd(const GroupedShape &s, int sms) {
-  GroupedFwdPlan p{};
-  const int64_t avg = s.T / s.E;
-  p.bands = cdiv(s.N, SmallmCfg<1>::BAND);
-  p.kc = static_cast<int>(cdiv(s.K, 256));
-  p.nt = s.T <= 8 ? 1 : (s.T <= 16 || avg <= 4 ? 2 : 4);
-  const int64_t tiles = token_tiles_bound(s.T, s.E, 8 * p.nt);
-  p.stream = avg <= kGroupedStreamTokens && tiles * p.bands * p.kc < (int64_t(1) << 30);
-  if (p.stream) {
-    p.grid = static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, tiles * p.bands * p.kc / 2), sms));
-    p.counters = tiles * p.bands;
-    p.part = align256(static_cast<size_t>(p.grid) * 2 * SmallmCfg<1>::WARPS * p.nt * 32 * 16);
-  } else {
-    p.ntt = avg >= kGroupedTwoSubtile ? 2 : 1;
-    p.slots = grouped_pair_slots(sms);
-    p.counters = 2 * p.slots;
-    p.part = grouped_part_bytes(p.slots, p.ntt, s.K / 64);
-  }
-  return p;
-}
-
-struct GroupedBwdPlan {
+struct GroupedPlanHost {
   int ntt, slots;
   int64_t counters;
   size_t part;
 };
-GroupedBwdPlan plan_grouped_bwd(const GroupedShape &s, int sms) {
-  GroupedBwdPlan p{};
+// kblocks: K / 64 (forward) or N / 64 (backward)
+GroupedPlanHost plan_grouped_host(const GroupedShape &s, int64_t kblocks, int sms) {
+  GroupedPlanHost p{};
   p.ntt = s.T / s.E >= kGroupedTwoSubtile ? 2 : 1;
   p.slots = grouped_pair_slots(sms);
   p.counters = 2 * p.slots;
-  p.part = grouped_part_bytes(p.slots, p.ntt, s.N / 64);
+  p.part = grouped_part_bytes(p.slots, p.ntt, kblocks);
   return p;
 }
 
@@ -282,7 +260,7 @@ qlora_status grouped_fwd(const uint8_t *packed, const uint8_t *q, const float *s
                          const float *t8, const GroupedShape &s, const int *offsets, const void *X, const void *A,
                          const void *B, float alpha, const DropoutArgs &drop, void *Y, void *XA_out, void *workspace,
                          size_t workspace_bytes, int sms, cudaStream_t cs) {
-  const GroupedFwdPlan p = plan_grouped_fwd(s, sms);
+  const GroupedPlanHost p = plan_grouped_host(s, s.K / 64, sms);
   const GroupedWs w = grouped_ws(s, p.counters, p.part, false);
   if (!workspace || workspace_bytes < w.total) return QLORA_ERR_WORKSPACE;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -299,36 +277,6 @@ qlora_status grouped_fwd(const uint8_t *packed, const uint8_t *q, const float *s
   if (st != QLORA_OK) return st;
 
   // 2) the base product, whose main loop overlaps 1)
-  if (p.stream) {
-    SmallmArgs a;
-    std::memset(&a, 0, sizeof a);
-    if (!map_x_blocks(&a.tm_x, X, s.T, s.K, static_cast<uint32_t>(8 * p.nt)) ||
-        !make_map(&a.tm_w, packed, MAP_U8, s.K / 2, s.E * s.N, s.K / 2, 128, SmallmCfg<1>::BAND, SW_128B))
-      return QLORA_ERR_CUDA;
-    a.q = q;
-    a.scale2 = scale2;
-    a.B = static_cast<const uint16_t *>(B);
-    a.xas = static_cast<const uint16_t *>(xas);
-    a.Y = static_cast<uint16_t *>(Y);
-    a.part = part;
-    a.counters = counters;
-    a.N = s.N;
-    a.K = s.K;
-    a.M = static_cast<int>(s.T);
-    a.r = s.r;
-    a.kc = p.kc;
-    a.tabs = make_tables(nf4, t8);
-    a.groups = g;
-    trace_begin(cs);
-    if (t_f16)
-      st = p.nt == 1 ? run_smallm_nt<1, true, true>(a, p.grid, cs)
-                     : p.nt == 2 ? run_smallm_nt<2, true, true>(a, p.grid, cs) : run_smallm_nt<4, true, true>(a, p.grid, cs);
-    else
-      st = p.nt == 1 ? run_smallm_nt<1, false, true>(a, p.grid, cs)
-                     : p.nt == 2 ? run_smallm_nt<2, false, true>(a, p.grid, cs) : run_smallm_nt<4, false, true>(a, p.grid, cs);
-    trace_end(cs);
-    return st;
-  }
   GemmArgs a;
   std::memset(&a, 0, sizeof a);
   const uint32_t box = static_cast<uint32_t>(128 * p.ntt);
@@ -347,7 +295,7 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
                          const float *t8, const GroupedShape &s, const int *offsets, const void *X, const void *dY,
                          const void *A, const void *B, const void *XA, float alpha, const DropoutArgs &drop, void *dX,
                          void *dA, void *dB, void *workspace, size_t workspace_bytes, int sms, cudaStream_t cs) {
-  const GroupedBwdPlan p = plan_grouped_bwd(s, sms);
+  const GroupedPlanHost p = plan_grouped_host(s, s.N / 64, sms);
   const GroupedWs w = grouped_ws(s, p.counters, p.part, true);
   if (!workspace || workspace_bytes < w.total) return QLORA_ERR_WORKSPACE;
   uint8_t *ws = static_cast<uint8_t *>(workspace);

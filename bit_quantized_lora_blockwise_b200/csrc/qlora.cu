@@ -664,17 +664,17 @@ qlora_status skinny(SkinnyKind kind, const void *aop, int64_t a_inner, int64_t a
 
 // -------------------------------------------------------- fused GEMMs --
 // The pair variants of the fused GEMM (256 weight rows x 256 tokens per
-// cluster of two CTAs): six token stages of one K block of 128 tokens (one
-// 16 KB TMA box each), dequantized-weight stages of one K block (16 KB) and
-// packed-code slots of 4 K blocks (18 KB).
+// cluster of two CTAs): five ring stages of one K block (a 16 KB box of tokens
+// and 16 KB of decoded weight), three packed-code slots of 4 K blocks, 16
+// dequant warps. (The codes come from HBM: two slots, or slots of 2 K blocks,
+// starve the dequant warps; 656 ns a job against 398.)
 constexpr int kPairBkb = 1, kPairSb = 5, kPairSa = 5, kPairSp = 3, kPairNpw = 16;
 using FwdPairCfg = GemmCfg<256, A_DEQ_K, L2_A_MN, kPairBkb, kPairSb, kPairSa, kPairSp, kPairNpw, true>;
 using BwdPairCfg = GemmCfg<256, A_DEQ_MN, L2_A_K, kPairBkb, kPairSb, kPairSa, kPairSp, kPairNpw, true>;
 // Two 256-token sub-tiles per job (512 tokens per tile, each CTA loading 256
-// of them): four token stages of one K block (32 KB boxes; finer stages than
-// two of two blocks hide a refill behind three stages of MMAs, 2-3 % faster
-// on the 7B shapes), 3 dequantized-weight stages, 2 packed-code slots (212 KB
-// of shared memory).
+// of them): four stages (a 32 KB box of tokens and 16 KB of decoded weight),
+// two packed-code slots of 2 K blocks, 12 dequant warps: a job takes the MMAs
+// 700 ns, so fewer codes in flight and fewer decoders keep up.
 constexpr int kPair2Bkb = 1, kPair2Sb = 4, kPair2Sa = 4, kPair2Sp = 2, kPair2Npw = 12;
 using FwdPair2Cfg = GemmCfg<256, A_DEQ_K, L2_A_MN, kPair2Bkb, kPair2Sb, kPair2Sa, kPair2Sp, kPair2Npw, true, 2>;
 using BwdPair2Cfg = GemmCfg<256, A_DEQ_MN, L2_A_K, kPair2Bkb, kPair2Sb, kPair2Sa, kPair2Sp, kPair2Npw, true, 2>;
@@ -799,20 +799,19 @@ int skinny_ctas(int64_t rows, int64_t kdim, int r) {
   return static_cast<int>(cdiv(rows, 128)) * p.splits;
 }
 
-template <int NT, bool F16, bool GROUPED = false>
+template <int NT, bool F16>
 qlora_status run_smallm_nt(const SmallmArgs &a, int grid, cudaStream_t st) {
-  using C = SmallmCfg<NT, GROUPED>;
+  using C = SmallmCfg<NT>;
   static std::once_flag once[kMaxDevices];
   int dev = 0;
   cudaGetDevice(&dev);
   cudaError_t attr_err = cudaSuccess;
   std::call_once(once[dev], [&] {
     attr_err =
-        cudaFuncSetAttribute(smallm_kernel<NT, F16, GROUPED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::SMEM_BYTES);
+        cudaFuncSetAttribute(smallm_kernel<NT, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   });
   if (attr_err != cudaSuccess) return QLORA_ERR_CUDA;
-  return launch_pdl(smallm_kernel<NT, F16, GROUPED>, grid, C::THREADS, C::SMEM_BYTES, st, a);
+  return launch_pdl(smallm_kernel<NT, F16>, grid, C::THREADS, C::SMEM_BYTES, st, a);
 }
 
 qlora_status run_smallm(const SmallmArgs &a, const SmallmPlan &p, cudaStream_t st) {
@@ -1749,8 +1748,7 @@ size_t qlora_grouped_workspace_bytes(int E, int64_t T, int64_t N, int64_t K, int
   DeviceInfo d;
   int sms = 148;
   if (device_info(&d) == QLORA_OK) sms = d.sms;
-  const GroupedFwdPlan f = plan_grouped_fwd(s, sms);
-  const GroupedBwdPlan b = plan_grouped_bwd(s, sms);
+  const GroupedPlanHost f = plan_grouped_host(s, K / 64, sms), b = plan_grouped_host(s, N / 64, sms);
   return std::max(grouped_ws(s, f.counters, f.part, false).total, grouped_ws(s, b.counters, b.part, true).total);
 }
 

@@ -37,18 +37,9 @@
 // pairs map to physical k 64t + 8u + 4h + {0,1} and {2,3}. One thread thus
 // decodes 64 consecutive codes of a row with one per-block bf16 table, and
 // reads the matching 8 bf16 of X with one 16-byte shared-memory load.
-//
-// Expert groups (GROUPED = true; groups.cuh). The weight is a stack of
-// experts [E N, K] and a band belongs to one (expert, token tile) pair: up to
-// 8 NT consecutive tokens of the expert. Experts without tokens have no
-// bands, so their weights are never read. The number of bands is known only
-// here, from the device offsets; the same even split then runs over the CTAs
-// that have work, and the others leave. NT = 4 (32 tokens in one pass over
-// the expert's codes) exists for groups only.
 #pragma once
 
 #include "codec.cuh"
-#include "groups.cuh"
 #include "ptx.cuh"
 
 namespace qlora {
@@ -68,10 +59,9 @@ struct SmallmArgs {
   int kc;     // 256-deep K chunks (the last may hold fewer than 4 blocks)
   int units;  // bands * kc
   CodecTables tabs;
-  GroupArgs groups;  // GROUPED only: units is then unused, M the tokens of all experts
 };
 
-template <int NT_, bool GROUPED_ = false>
+template <int NT_>
 struct SmallmCfg {
   static constexpr int NT = NT_;                 // 8-token MMA column tiles
   static constexpr int WARPS = 16;               // compute warps, one 16-row tile each
@@ -81,13 +71,12 @@ struct SmallmCfg {
   static constexpr int W_BYTES = BAND * 128;     // [256 rows][128 bytes = 256 codes]
   static constexpr int X_BYTES = 4 * XR * 128;   // [XR tokens][4 blocks][64 bf16]
   static constexpr int STAGE = W_BYTES + X_BYTES;
-  static constexpr int SX = NT == 1 ? 6 : (NT == 2 ? 5 : 4);  // stages
+  static constexpr int SX = NT == 1 ? 6 : 5;     // stages
   static constexpr int OFF_BAR = SX * STAGE;
   // full[SX] empty[SX], then the CTA's group barrier (one arrival per warp)
   static constexpr int OFF_T8 = OFF_BAR + (2 * SX + 2) * 8;
   static constexpr int OFF_MISC = OFF_T8 + 256 * 4;  // abort flag, two completed-band flags
-  static constexpr int OFF_GROUPS = OFF_MISC + 16;
-  static constexpr int SMEM_BYTES = OFF_GROUPS + (GROUPED_ ? kGroupTableBytes : 0);
+  static constexpr int SMEM_BYTES = OFF_MISC + 16;
   static constexpr int SLOT_FLOATS = WARPS * NT * 32 * 4;
   static_assert(W_BYTES % 1024 == 0 && X_BYTES % 1024 == 0, "stages keep the 1024-byte swizzle alignment");
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
@@ -102,9 +91,9 @@ __host__ __device__ __forceinline__ int smallm_unit_begin(int64_t cta, int64_t u
   return static_cast<int>(cta * units / grid);
 }
 
-template <int NT, bool F16, bool GROUPED = false>
+template <int NT, bool F16>
 __global__ void __launch_bounds__(SmallmCfg<NT>::THREADS, 1) smallm_kernel(const __grid_constant__ SmallmArgs a) {
-  using C = SmallmCfg<NT, GROUPED>;
+  using C = SmallmCfg<NT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -114,52 +103,10 @@ __global__ void __launch_bounds__(SmallmCfg<NT>::THREADS, 1) smallm_kernel(const
   auto empty_bar = [&](int s) { return sbase + C::OFF_BAR + 8u * (C::SX + s); };
   const uint32_t group_bar = sbase + C::OFF_BAR + 8u * (2 * C::SX);
 
-  int grid = gridDim.x;
-  int total = a.units;
-  const GroupTable gt = group_table(smem + C::OFF_GROUPS);
-  const int bands = static_cast<int>((a.N + C::BAND - 1) / C::BAND);  // per expert and token tile
-  if constexpr (GROUPED) {
-    if (warp == 0) build_group_table(a.groups, 8 * NT, gt);
-    __syncthreads();
-    total = gt.cum[a.groups.groups] * bands * a.kc;
-    // at least two units per CTA, as the host plans a dense call
-    const int want = total / 2 > 1 ? total / 2 : 1;
-    if (want < grid) grid = want;
-    if (total == 0 || static_cast<int>(blockIdx.x) >= grid) {
-      // the launch after this one may start before this grid ends only once
-      // the launch before it is complete
-      grid_dep_wait();
-      return;
-    }
-  }
-  const int u_begin = smallm_unit_begin(blockIdx.x, total, grid);
-  const int u_end = smallm_unit_begin(blockIdx.x + 1, total, grid);
+  const int grid = gridDim.x;
+  const int u_begin = smallm_unit_begin(blockIdx.x, a.units, grid);
+  const int u_end = smallm_unit_begin(blockIdx.x + 1, a.units, grid);
   const int nunits = u_end - u_begin;
-  // A band: its first row within the expert, the expert's first weight row
-  // and number, its tokens.
-  struct Band {
-    int64_t n0, w0;
-    int group, tok0, ntok;
-  };
-  auto band_at = [&](int b) {
-    Band d;
-    if constexpr (GROUPED) {
-      const int tt = b / bands;
-      d.group = group_of_tile(gt, a.groups.groups, tt);
-      d.n0 = static_cast<int64_t>(b - tt * bands) * C::BAND;
-      d.w0 = static_cast<int64_t>(d.group) * a.N;
-      d.tok0 = gt.first[d.group] + (tt - gt.cum[d.group]) * (8 * NT);
-      const int left = gt.first[d.group + 1] - d.tok0;
-      d.ntok = left < 8 * NT ? left : 8 * NT;
-    } else {
-      d.group = 0;
-      d.n0 = static_cast<int64_t>(b) * C::BAND;
-      d.w0 = 0;
-      d.tok0 = 0;
-      d.ntok = a.M;
-    }
-    return d;
-  };
 
   // Stage copies (lane 0 of warp 0): unit j goes to stage j % SX once every
   // warp has released unit j - SX; its codes (one box) and activations (one
@@ -182,14 +129,8 @@ __global__ void __launch_bounds__(SmallmCfg<NT>::THREADS, 1) smallm_kernel(const
       }
       const uint32_t dst = sbase + st * C::STAGE;
       mbar_arrive_expect_tx(full_bar(st), C::STAGE);
-      if constexpr (GROUPED) {
-        const Band d = band_at(is_band);
-        tma_load_2d(dst, &a.tm_w, full_bar(st), is_c * 128, static_cast<int>(d.w0 + d.n0));
-        tma_load_3d(dst + C::W_BYTES, &a.tm_x, full_bar(st), 0, is_c * 4, d.tok0);
-      } else {
-        tma_load_2d(dst, &a.tm_w, full_bar(st), is_c * 128, is_band * C::BAND);
-        tma_load_3d(dst + C::W_BYTES, &a.tm_x, full_bar(st), 0, is_c * 4, 0);
-      }
+      tma_load_2d(dst, &a.tm_w, full_bar(st), is_c * 128, is_band * C::BAND);
+      tma_load_3d(dst + C::W_BYTES, &a.tm_x, full_bar(st), 0, is_c * 4, 0);
       if (++is_c == a.kc) {
         is_c = 0;
         ++is_band;
@@ -223,21 +164,19 @@ __global__ void __launch_bounds__(SmallmCfg<NT>::THREADS, 1) smallm_kernel(const
     float s[2];
   };
   int ld_band = u_begin / a.kc, ld_c = u_begin - (u_begin / a.kc) * a.kc;
-  Band ld_at = band_at(ld_band);
   auto load_consts = [&](Consts &f) {
-    const int64_t row = ld_at.n0 + warp * 16 + g;
+    const int64_t row = static_cast<int64_t>(ld_band) * C::BAND + warp * 16 + g;
     const int64_t kb = static_cast<int64_t>(ld_c) * 4 + t;
 #pragma unroll
     for (int rr = 0; rr < 2; ++rr) {
       const bool ok = row + 8 * rr < a.N && kb < kb_total;
-      const int64_t bi = (ld_at.w0 + row + 8 * rr) * kb_total + kb;
+      const int64_t bi = (row + 8 * rr) * kb_total + kb;
       f.q[rr] = ok ? __ldg(a.q + bi) : 0u;
       f.s[rr] = ok ? __ldg(a.scale2 + (bi >> 8)) : 0.0f;  // c' = 0: the block contributes zeros
     }
     if (++ld_c == a.kc) {
       ld_c = 0;
       ++ld_band;
-      if (ld_band * a.kc < u_end) ld_at = band_at(ld_band);
     }
   };
 
@@ -255,9 +194,8 @@ __global__ void __launch_bounds__(SmallmCfg<NT>::THREADS, 1) smallm_kernel(const
     uint32_t af[4][4];
     uint32_t bf[4][NT][2];
   };
-  auto adapter = [&](const Band &d) { return a.B + static_cast<int64_t>(d.group) * a.r * a.N; };
-  auto lora_load = [&](const Band &d, int64_t n0, int j00, LoraFrag &L) {
-    const uint16_t *Bh = adapter(d);
+  auto lora_load = [&](int64_t n0, int j00, LoraFrag &L) {
+    const uint16_t *Bh = reinterpret_cast<const uint16_t *>(a.B);
     auto bval = [&](int j, int64_t n) -> uint32_t { return j < a.r ? Bh[static_cast<int64_t>(j) * a.N + n] : 0u; };
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -269,9 +207,9 @@ __global__ void __launch_bounds__(SmallmCfg<NT>::THREADS, 1) smallm_kernel(const
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int m = 8 * nt + g;
-        const uint32_t *xr = reinterpret_cast<const uint32_t *>(a.xas + static_cast<int64_t>(d.tok0 + m) * a.r);
-        L.bf[q][nt][0] = (m < d.ntok && ja < a.r) ? xr[ja >> 1] : 0u;
-        L.bf[q][nt][1] = (m < d.ntok && jb < a.r) ? xr[jb >> 1] : 0u;
+        const uint32_t *xr = reinterpret_cast<const uint32_t *>(a.xas + static_cast<int64_t>(m) * a.r);
+        L.bf[q][nt][0] = (m < a.M && ja < a.r) ? xr[ja >> 1] : 0u;
+        L.bf[q][nt][1] = (m < a.M && jb < a.r) ? xr[jb >> 1] : 0u;
       }
     }
   };
@@ -282,34 +220,35 @@ __global__ void __launch_bounds__(SmallmCfg<NT>::THREADS, 1) smallm_kernel(const
       for (int nt = 0; nt < NT; ++nt)
         mma_16816<F16>(acc[nt], L.af[q][0], L.af[q][1], L.af[q][2], L.af[q][3], L.bf[q][nt][0], L.bf[q][nt][1]);
   };
-  auto store_y = [&](const Band &d, int64_t n0) {
+  auto band_row0 = [&](int band) { return static_cast<int64_t>(band) * C::BAND + warp * 16; };
+  auto store_y = [&](int64_t n0) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int m = 8 * nt + 2 * t + (e & 1);
         const int64_t n = n0 + g + 8 * (e >> 1);
-        if (m < d.ntok) a.Y[static_cast<int64_t>(d.tok0 + m) * a.N + n] = to_16(acc[nt][e], F16);
+        if (m < a.M) a.Y[static_cast<int64_t>(m) * a.N + n] = to_16(acc[nt][e], F16);
       }
   };
   // after the stream (registers free): first 64 ranks preloaded
-  auto epilogue = [&](const Band &d, const LoraFrag &L0) {
-    const int64_t n0 = d.n0 + warp * 16;
+  auto epilogue = [&](int band, const LoraFrag &L0) {
+    const int64_t n0 = band_row0(band);
     if (n0 >= a.N) return;
     lora_apply(L0);
     for (int j00 = 64; j00 < a.r; j00 += 64) {
       LoraFrag L;
-      lora_load(d, n0, j00, L);
+      lora_load(n0, j00, L);
       lora_apply(L);
     }
-    store_y(d, n0);
+    store_y(n0);
   };
   // inside the stream (the next unit's loads hold registers): one 16-rank
   // step at a time
-  auto epilogue_lean = [&](const Band &d) {
-    const int64_t n0 = d.n0 + warp * 16;
+  auto epilogue_lean = [&](int band) {
+    const int64_t n0 = band_row0(band);
     if (n0 >= a.N) return;
-    const uint16_t *Bh = adapter(d);
+    const uint16_t *Bh = reinterpret_cast<const uint16_t *>(a.B);
     auto bval = [&](int j, int64_t n) -> uint32_t { return j < a.r ? Bh[static_cast<int64_t>(j) * a.N + n] : 0u; };
 #pragma unroll 1
     for (int j0 = 0; j0 < a.r; j0 += 16) {
@@ -321,13 +260,13 @@ __global__ void __launch_bounds__(SmallmCfg<NT>::THREADS, 1) smallm_kernel(const
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int m = 8 * nt + g;
-        const uint32_t *xr = reinterpret_cast<const uint32_t *>(a.xas + static_cast<int64_t>(d.tok0 + m) * a.r);
-        const uint32_t b0 = (m < d.ntok && ja < a.r) ? xr[ja >> 1] : 0u;
-        const uint32_t b1 = (m < d.ntok && jb < a.r) ? xr[jb >> 1] : 0u;
+        const uint32_t *xr = reinterpret_cast<const uint32_t *>(a.xas + static_cast<int64_t>(m) * a.r);
+        const uint32_t b0 = (m < a.M && ja < a.r) ? xr[ja >> 1] : 0u;
+        const uint32_t b1 = (m < a.M && jb < a.r) ? xr[jb >> 1] : 0u;
         mma_16816<F16>(acc[nt], a0, a1, a2, a3, b0, b1);
       }
     }
-    store_y(d, n0);
+    store_y(n0);
   };
   // Partial slots of CTA `cta`: 0 holds the piece of the band its range
   // starts in (when an earlier CTA started that band), 1 the piece of the
@@ -351,7 +290,6 @@ __global__ void __launch_bounds__(SmallmCfg<NT>::THREADS, 1) smallm_kernel(const
   const uint32_t swz16 = static_cast<uint32_t>(((4 * g + t) & 7) << 4);
   const uint32_t xrow = sbase + C::W_BYTES + static_cast<uint32_t>((4 * g + t) * 128);
   int cur_band = u_begin / a.kc, cur_c = u_begin - (u_begin / a.kc) * a.kc, piece0 = u_begin;
-  Band cur_at = band_at(cur_band);
   // Decode one unit's codes into MMA fragments and accumulate; then
   // release its stage and close the piece if a band ends.
   auto run_unit = [&](int i, const Consts &f) -> bool {
@@ -361,7 +299,7 @@ __global__ void __launch_bounds__(SmallmCfg<NT>::THREADS, 1) smallm_kernel(const
     if (warp == 0 && lane == 0) issue(i);
     __syncwarp();
     if (!__all_sync(0xFFFFFFFFu, mbar_wait_spin(full_bar(s), (i / C::SX) & 1u, s_abort))) return false;
-    const bool rows_here = cur_at.n0 + warp * 16 < a.N;
+    const bool rows_here = static_cast<int64_t>(cur_band) * C::BAND + warp * 16 < a.N;
     if (rows_here) {
       const Nf4Planes P0 = make_planes(a.tabs.nf4, cp0, F16);
       const Nf4Planes P1 = make_planes(a.tabs.nf4, cp1, F16);
@@ -389,11 +327,9 @@ __global__ void __launch_bounds__(SmallmCfg<NT>::THREADS, 1) smallm_kernel(const
     if (lane == 0) mbar_arrive(empty_bar(s));
     const int u = u_begin + i;
     const int band = cur_band;
-    const Band done = cur_at;
     if (++cur_c == a.kc) {
       cur_c = 0;
       ++cur_band;
-      if (i + 1 < nunits) cur_at = band_at(cur_band);
     }
     if (i + 1 == nunits || cur_c == 0) {
       const int64_t first_u = static_cast<int64_t>(band) * a.kc;
@@ -403,7 +339,7 @@ __global__ void __launch_bounds__(SmallmCfg<NT>::THREADS, 1) smallm_kernel(const
           grid_dep_wait();  // X A of this call is ready
           waited = true;
         }
-        epilogue_lean(done);
+        epilogue_lean(band);
       } else {
         // a piece of a band shared with other CTAs: park it; the CTA whose
         // piece completes the band sums them all (after the stream)
@@ -468,7 +404,7 @@ __global__ void __launch_bounds__(SmallmCfg<NT>::THREADS, 1) smallm_kernel(const
       int last = 0;
       if (band >= 0) {
         const int64_t first_u = static_cast<int64_t>(band) * a.kc;
-        const int npieces = smallm_cta_of(first_u + a.kc - 1, total, grid) - smallm_cta_of(first_u, total, grid) + 1;
+        const int npieces = smallm_cta_of(first_u + a.kc - 1, a.units, grid) - smallm_cta_of(first_u, a.units, grid) + 1;
         const unsigned int prev = atomicAdd(&a.counters[band], 1u);
         last = prev == static_cast<unsigned int>(npieces - 1);
         if (last) a.counters[band] = 0u;  // every piece is in: left zero for the next call
@@ -483,11 +419,10 @@ __global__ void __launch_bounds__(SmallmCfg<NT>::THREADS, 1) smallm_kernel(const
     if (band < 0 || !s_last[k]) continue;
     __threadfence();
     const int64_t first_u = static_cast<int64_t>(band) * a.kc;
-    const int c0 = smallm_cta_of(first_u, total, grid);
-    const int c1 = smallm_cta_of(first_u + a.kc - 1, total, grid);
+    const int c0 = smallm_cta_of(first_u, a.units, grid);
+    const int c1 = smallm_cta_of(first_u + a.kc - 1, a.units, grid);
     LoraFrag L0;  // its loads overlap the slot loads below
-    const Band at = band_at(band);
-    if (at.n0 + warp * 16 < a.N) lora_load(at, at.n0 + warp * 16, 0, L0);
+    if (band_row0(band) < a.N) lora_load(band_row0(band), 0, L0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -513,7 +448,7 @@ __global__ void __launch_bounds__(SmallmCfg<NT>::THREADS, 1) smallm_kernel(const
           }
         }
     }
-    epilogue(at, L0);
+    epilogue(band, L0);
   }
 }
 

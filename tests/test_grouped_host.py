@@ -97,7 +97,8 @@ def test_workspace_query(lib):
     assert ws(4, 0, 128, 128, 8) > 0
     plain = ws(4, 1000, 1024, 2048, 8)
     assert plain >= 2 * 1000 * 8 * 2
-    assert ws(4, 1000, 1024, 2048, 8, True) >= plain + 1000 * 2048 * 2 - (1 << 20) > plain
+    # the mask is never stored and X never copied: dropout needs no scratch of its own
+    assert ws(4, 1000, 1024, 2048, 8, True) == plain
 
 
 def test_binding_refusals(lib):
