@@ -192,7 +192,7 @@ def _ptr(t) -> ctypes.c_void_p | None:
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _req(t, name, dtype, shape=None):
@@ -521,10 +521,9 @@ def dropout(x: torch.Tensor, drop: Dropout, out=None) -> torch.Tensor:
     _req(x, "x", x.dtype)
     if out is None:
         out = torch.empty_like(x)
-    _req(out, "out", x.dtype, tuple(x.shape))
-    _same_device(x, out=out)
-    with torch.cuda.device(x.device):
-        _check(load().qlora_dropout(_ptr(x), _ptr(out), x.numel(), _ELEMENT[x.dtype], drop._desc(), _stream()),
+    _need(out, "out", x.dtype, x.shape, x.device)
+    with _on(x.device):
+        _check(load().qlora_dropout(x.data_ptr(), out.data_ptr(), x.numel(), _ELEMENT[x.dtype], drop._desc(), _stream()),
                "qlora_dropout")
     return out
 
@@ -535,10 +534,35 @@ def grouped_workspace_bytes(E: int, T: int, N: int, K: int, r: int, dropout: boo
     return int(load().qlora_grouped_workspace_bytes(E, T, N, K, r, 1 if dropout else 0))
 
 
-def _same_device(ref, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+def _need(t, name, dtype, shape, device):
+    """_req and the device, with one quick test of the ordinary case (the
+    grouped calls take a dozen tensors and can be shorter than their checks)."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous() and t.is_cuda):
+        return t
+    _req(t, name, dtype, shape)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t
+
+
+class _on:
+    """The device of a call made current for its duration, at no cost where it already is."""
+
+    def __init__(self, device):
+        self.ctx = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _dense_adapters(A, B, N, K):
@@ -558,64 +582,62 @@ def _expert_adapters(A, B, N, K):
 
 def _grouped_checks(packed, q, scale2, X, offsets, A, B, N, K, workspace, drop, shapes):
     E, r, a_shape, b_shape = shapes
-    T = X.shape[0]
     dt = _dtype_of(X, "X")
-    _req(packed, "packed", torch.uint8, (E * N * K // 2,))
-    _req(q, "q", torch.uint8, (E * N * K // BLOCK,))
-    _req(scale2, "scale2", torch.float32, (-(-(E * N * K // BLOCK) // DQ_BLOCK),))
+    T, dev = X.shape[0], X.device
+    blocks = E * N * K // BLOCK
     _req(X, "X", dt, (T, K))
-    _req(A, "A", dt, a_shape)
-    _req(B, "B", dt, b_shape)
+    _need(packed, "packed", torch.uint8, (E * N * K // 2,), dev)
+    _need(q, "q", torch.uint8, (blocks,), dev)
+    _need(scale2, "scale2", torch.float32, (-(-blocks // DQ_BLOCK),), dev)
+    _need(A, "A", dt, a_shape, dev)
+    _need(B, "B", dt, b_shape, dev)
     if offsets is not None:
-        _req(offsets, "offsets", torch.int32, (E + 1,))
+        _need(offsets, "offsets", torch.int32, (E + 1,), dev)
     if workspace is None:
         need = grouped_workspace_bytes(E, T, N, K, r, drop is not None)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=X.device)
-    _req(workspace, "workspace", torch.uint8)
-    _same_device(X, packed=packed, q=q, scale2=scale2, offsets=offsets, A=A, B=B, workspace=workspace)
-    return E, T, r, dt, workspace
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    return E, T, r, dt, dev, workspace
 
 
 def _grouped_fwd(packed, q, scale2, X, offsets, A, B, alpha, N, K, drop, nf4, t8, Y, XA_out, workspace, shapes):
-    E, T, r, dt, workspace = _grouped_checks(packed, q, scale2, X, offsets, A, B, N, K, workspace, drop, shapes)
+    E, T, r, dt, dev, workspace = _grouped_checks(packed, q, scale2, X, offsets, A, B, N, K, workspace, drop, shapes)
     if Y is None:
         # rows that no expert owns are left as they are: zeros in a buffer made here
-        Y = (torch.zeros if offsets is not None else torch.empty)((T, N), dtype=dt, device=X.device)
-    _req(Y, "Y", dt, (T, N))
+        Y = (torch.zeros if offsets is not None else torch.empty)((T, N), dtype=dt, device=dev)
+    _need(Y, "Y", dt, (T, N), dev)
     if XA_out is not None:
-        _req(XA_out, "XA_out", dt, (T, r))
-    _same_device(X, Y=Y, XA_out=XA_out)
+        _need(XA_out, "XA_out", dt, (T, r), dev)
     tb = _tables(nf4, t8)
-    with torch.cuda.device(X.device):
-        _check(load().qlora_grouped_linear_fwd(_ptr(packed), _ptr(q), _ptr(scale2), tb.nf4, tb.t8, _DTYPE[dt], E, T, N,
-                                               K, _ptr(offsets), _ptr(X), _ptr(A), _ptr(B), r, float(alpha),
-                                               None if drop is None else drop._desc(), _ptr(Y), _ptr(XA_out),
-                                               _ptr(workspace), workspace.numel(), _stream()),
-               "qlora_grouped_linear_fwd")
+    with _on(dev):
+        _check(load().qlora_grouped_linear_fwd(
+            packed.data_ptr(), q.data_ptr(), scale2.data_ptr(), tb.nf4, tb.t8, _DTYPE[dt], E, T, N, K, _addr(offsets),
+            X.data_ptr(), A.data_ptr(), B.data_ptr(), r, float(alpha), None if drop is None else drop._desc(),
+            Y.data_ptr(), _addr(XA_out), workspace.data_ptr(), workspace.numel(), _stream()),
+            "qlora_grouped_linear_fwd")
     return Y
 
 
 def _grouped_bwd(packed, q, scale2, X, dY, offsets, A, B, alpha, N, K, XA, drop, nf4, t8, dX, dA, dB, workspace,
                  shapes):
-    E, T, r, dt, workspace = _grouped_checks(packed, q, scale2, X, offsets, A, B, N, K, workspace, drop, shapes)
-    _req(dY, "dY", dt, (T, N))
+    E, T, r, dt, dev, workspace = _grouped_checks(packed, q, scale2, X, offsets, A, B, N, K, workspace, drop, shapes)
+    _need(dY, "dY", dt, (T, N), dev)
     if XA is not None:
-        _req(XA, "XA", dt, (T, r))
+        _need(XA, "XA", dt, (T, r), dev)
     if dX is None:
-        dX = (torch.zeros if offsets is not None else torch.empty)((T, K), dtype=dt, device=X.device)
+        dX = (torch.zeros if offsets is not None else torch.empty)((T, K), dtype=dt, device=dev)
     dA = torch.empty_like(A) if dA is None else dA
     dB = torch.empty_like(B) if dB is None else dB
-    _req(dX, "dX", dt, (T, K))
-    _req(dA, "dA", dt, tuple(A.shape))
-    _req(dB, "dB", dt, tuple(B.shape))
-    _same_device(X, dY=dY, XA=XA, dX=dX, dA=dA, dB=dB)
+    _need(dX, "dX", dt, (T, K), dev)
+    _need(dA, "dA", dt, A.shape, dev)
+    _need(dB, "dB", dt, B.shape, dev)
     tb = _tables(nf4, t8)
-    with torch.cuda.device(X.device):
-        _check(load().qlora_grouped_linear_bwd(_ptr(packed), _ptr(q), _ptr(scale2), tb.nf4, tb.t8, _DTYPE[dt], E, T, N,
-                                               K, _ptr(offsets), _ptr(X), _ptr(dY), _ptr(A), _ptr(B), _ptr(XA), r,
-                                               float(alpha), None if drop is None else drop._desc(), _ptr(dX), _ptr(dA),
-                                               _ptr(dB), _ptr(workspace), workspace.numel(), _stream()),
-               "qlora_grouped_linear_bwd")
+    with _on(dev):
+        _check(load().qlora_grouped_linear_bwd(
+            packed.data_ptr(), q.data_ptr(), scale2.data_ptr(), tb.nf4, tb.t8, _DTYPE[dt], E, T, N, K, _addr(offsets),
+            X.data_ptr(), dY.data_ptr(), A.data_ptr(), B.data_ptr(), _addr(XA), r, float(alpha),
+            None if drop is None else drop._desc(), dX.data_ptr(), dA.data_ptr(), dB.data_ptr(), workspace.data_ptr(),
+            workspace.numel(), _stream()), "qlora_grouped_linear_bwd")
     return dX, dA, dB
 
 

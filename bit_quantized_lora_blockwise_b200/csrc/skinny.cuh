@@ -30,12 +30,13 @@
 //
 // Adapter dropout (DROP = true): the product reads M o X in place of X (kept
 // elements as they are; the factor is in the output's scale). X never makes
-// a pass of its own: warps 4-7, idle until the readout, take each landed
+// a pass of its own: warps 4-11, idle until the readout, take each landed
 // 16 KB stage of X through the mask in shared memory before the MMAs read
-// it, 16 bytes (8 elements, one Philox counter) at a time. Bound by that
-// integer work, about 1000 clocks a stage and SM, 4.5 TB/s of X. (A dropout
-// launch ahead of the product wrote and re-read X: 840 us against 777 for the
-// whole backward of 8192 rows through 4096 x 11008.)
+// it, 16 bytes (8 elements, one Philox counter) at a time. (A dropout launch
+// ahead of the product wrote and re-read X: 840 us against 777 for the whole
+// backward of 8192 rows through 4096 x 11008; with four masking warps, whose
+// latency a stage then waits for, that last launch trailed dX by 130 us,
+// with eight by 97.)
 #pragma once
 
 #include "codec.cuh"
@@ -96,7 +97,7 @@ struct SkinnyCfg {
   static constexpr int OFF_MISC = (OFF_BAR + NBARS * 8 + 15) & ~15;
   static constexpr int OFF_GROUPS = OFF_MISC + 16;
   static constexpr int SMEM_BYTES = OFF_GROUPS + (GROUPED_ ? kGroupTableBytes : 0);
-  static constexpr int THREADS = 256;
+  static constexpr int THREADS = DROP_ ? 384 : 256;  // DROP: warps 8-11 mask beside warps 4-7
   static constexpr uint32_t TMEM_COLS = BN_ <= 64 ? 64 : (BN_ <= 128 ? 128 : 256);
   static constexpr int PART_LD = BN_ + 4;  // fp32 per partial row (16-byte pad against bank conflicts)
   static_assert(128 * PART_LD * 4 <= OFF_BAR, "the partial reuses the ring");
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
       mbar_init(landed_bar, 1);
       mbar_init(tail_bar, 1);
     }
-    for (int s = 0; s < C::STAGES && C::DROP; ++s) mbar_init(ready_bar(s), 4);
+    for (int s = 0; s < C::STAGES && C::DROP; ++s) mbar_init(ready_bar(s), 8);
     *s_abort = 0;
     fence_barrier_init();
   }
@@ -312,26 +313,26 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
     if constexpr (C::DROP) {
       // M o X, stage by stage. 16-byte piece c of row r of a 64-wide K-major
       // (or MN-major) chunk lies at c ^ (r & 7) in the row's 128 bytes. A
-      // thread's eight pieces are 16 rows apart; their masks are formed side
+      // thread's four pieces are 32 rows apart; their masks are formed side
       // by side before the stage is waited for. Rows of no token of this
       // expert are masked too: never stored (K-major) or zeroed by warp 2.
       const int tid = q * 32 + lane, c = tid & 7, r0 = tid >> 3;
-      const uint32_t swz = static_cast<uint32_t>(c ^ (r0 & 7)) << 4;  // (the same for rows 16 apart)
+      const uint32_t swz = static_cast<uint32_t>(c ^ (r0 & 7)) << 4;  // (the same for rows 32 apart)
       const uint64_t ld8 = static_cast<uint64_t>(args.drop_ld) / 8;
       for (int j = 0; P.masked && j < nk; ++j) {
         const int s = j % C::STAGES, kb = kb_begin + j;
         // counter of the piece in row r0: K-major 128 token rows of one chunk, MN-major 64 token rows of two
         const uint64_t first = C::A_MN ? static_cast<uint64_t>(tok0 + kb * 64 + r0) * ld8 + (row0 / 8 + c)
                                        : static_cast<uint64_t>(row0 + r0) * ld8 + (kb * 8 + c);
-        uint4 mask[8];
+        uint4 mask[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          mask[i] = dropout_mask8(args.drop, first + (C::A_MN ? (i & 3) * 16 * ld8 + (i >> 2) * 8 : i * 16 * ld8));
+        for (int i = 0; i < 4; ++i)
+          mask[i] = dropout_mask8(args.drop, first + (C::A_MN ? (i & 1) * 32 * ld8 + (i >> 1) * 8 : i * 32 * ld8));
         if (!warp_wait_all(full_bar(s), (j / C::STAGES) & 1u, s_abort)) break;
         uint8_t *piece = smem + C::OFF_A + s * C::A_BYTES + r0 * 128 + swz;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint4 *at = reinterpret_cast<uint4 *>(piece + i * 2048);
+        for (int i = 0; i < 4; ++i) {
+          uint4 *at = reinterpret_cast<uint4 *>(piece + i * 4096);
           const uint4 v = *at;
           *at = make_uint4(v.x & mask[i].x, v.y & mask[i].y, v.z & mask[i].z, v.w & mask[i].w);
         }
@@ -344,12 +345,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
     const bool ok = (!C::GROUPED || nk > 0) && warp_wait_all(tmem_full, 0, s_abort);
     tc_fence_after();
     float *part = reinterpret_cast<float *>(smem);
-    const int lrow = q * 32 + lane;
+    const int lrow = (q & 3) * 32 + lane;
 #pragma unroll 1
-    for (int ch = 0; ch < C::BN / 32; ++ch) {
+    for (int ch = q >> 2; ch < C::BN / 32; ch += C::THREADS / 128 - 1) {
       uint32_t u[32];
       if (ok && nk > 0) {
-        tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + ch * 32, u);
+        tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>((q & 3) * 32) << 16) + ch * 32, u);
       } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j) u[j] = 0u;
