@@ -19,7 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libqlora.so")
 SOURCES = ["qlora.cu", "codec.cuh", "gemm.cuh", "skinny.cuh", "smallm.cuh", "adamw.cuh", "ptx.cuh",
-           "groups.cuh", "dropout.cuh", "grouped_host.cuh"]
+           "groups.cuh", "dropout.cuh", "gradients.cuh", "grouped_host.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -17,41 +17,51 @@
 namespace qlora {
 
 struct DropoutArgs {
-  uint64_t seed;
+  uint32_t key[10][2];  // the rounds' keys, formed once on the host: constant operands of the rounds' xors
   uint64_t offset;
   uint32_t threshold;  // 0: nothing is dropped
   float factor;        // 2^16 / (2^16 - threshold)
 };
 
-// The eight halves of one counter, two per word.
-__device__ __forceinline__ uint4 philox4x32_10(uint64_t seed, uint64_t counter) {
-  uint32_t c0 = static_cast<uint32_t>(counter), c1 = static_cast<uint32_t>(counter >> 32), c2 = 0u, c3 = 0u;
+inline DropoutArgs dropout_args(uint64_t seed, uint64_t offset, uint32_t threshold) {
+  DropoutArgs d;
   uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+  for (int round = 0; round < 10; ++round, k0 += 0x9E3779B9u, k1 += 0xBB67AE85u) {
+    d.key[round][0] = k0;
+    d.key[round][1] = k1;
+  }
+  d.offset = offset;
+  d.threshold = threshold;
+  d.factor = static_cast<float>(65536.0 / (65536.0 - threshold));
+  return d;
+}
+
+// The eight halves of one counter, two per word.
+__device__ __forceinline__ uint4 philox4x32_10(const DropoutArgs &d, uint64_t counter) {
+  uint32_t c0 = static_cast<uint32_t>(counter), c1 = static_cast<uint32_t>(counter >> 32), c2 = 0u, c3 = 0u;
 #pragma unroll
   for (int round = 0; round < 10; ++round) {
     const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u;
     const uint64_t b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-    const uint32_t n0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
-    const uint32_t n2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+    const uint32_t n0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ d.key[round][0];
+    const uint32_t n2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ d.key[round][1];
     c1 = static_cast<uint32_t>(b);
     c3 = static_cast<uint32_t>(a);
     c0 = n0;
     c2 = n2;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   return make_uint4(c0, c1, c2, c3);
 }
 
-// Whether the elements of a word's low and high half are kept: both 16-bit
-// compares in one packed maximum, whose predicates are half >= threshold.
+// Whether the elements of a word's low and high half are kept.
 __device__ __forceinline__ void keep_pair(uint32_t word, uint32_t threshold, bool &lo, bool &hi) {
-  __vibmax_u16x2(word, threshold * 0x10001u, &hi, &lo);
+  hi = word >= threshold << 16;
+  lo = word << 16 >= threshold << 16;
 }
 
 // Keep bits of the eight elements of one counter (bit j: element j).
 __device__ __forceinline__ uint32_t dropout_keep8(const DropoutArgs &d, uint64_t group) {
-  const uint4 w = philox4x32_10(d.seed, d.offset + group);
+  const uint4 w = philox4x32_10(d, d.offset + group);
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   uint32_t keep = 0u;
 #pragma unroll
@@ -65,7 +75,7 @@ __device__ __forceinline__ uint32_t dropout_keep8(const DropoutArgs &d, uint64_t
 
 // The same as masks of the four words of eight 16-bit elements.
 __device__ __forceinline__ uint4 dropout_mask8(const DropoutArgs &d, uint64_t group) {
-  const uint4 w = philox4x32_10(d.seed, d.offset + group);
+  const uint4 w = philox4x32_10(d, d.offset + group);
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   uint32_t m[4];
 #pragma unroll
@@ -101,7 +111,7 @@ __device__ __forceinline__ uint32_t dropout_pair(uint32_t v, bool klo, bool khi,
 // The same for the eight elements of one counter.
 template <int TYPE>
 __device__ __forceinline__ uint4 dropout_eight(const uint4 &v, const DropoutArgs &d, uint64_t group, float factor) {
-  const uint4 w = philox4x32_10(d.seed, d.offset + group);
+  const uint4 w = philox4x32_10(d, d.offset + group);
   const uint32_t u[4] = {w.x, w.y, w.z, w.w}, x[4] = {v.x, v.y, v.z, v.w};
   uint32_t y[4];
 #pragma unroll
@@ -117,7 +127,8 @@ __device__ __forceinline__ uint4 dropout_eight(const uint4 &v, const DropoutArgs
 // aligned, y == x allowed. One thread per counter (8 elements: one 16-byte
 // load and store for 16-bit types, two for fp32).
 template <int TYPE>
-__global__ void __launch_bounds__(256) dropout_kernel(const void *x, void *y, int64_t n, const DropoutArgs d) {
+__global__ void __launch_bounds__(256) dropout_kernel(const void *x, void *y, int64_t n,
+                                                      const __grid_constant__ DropoutArgs d) {
   const float factor = d.factor;
   grid_dep_wait();
   grid_dep_launch();

@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
           if (tok - lane >= end) continue;
           const uint64_t group = (static_cast<uint64_t>(tok) * args.out_ld + base) / 8;
           uint32_t word = 0u;
-#pragma unroll 1
+#pragma unroll
           for (int j = 0; j < 4; ++j) word |= dropout_keep8(args.drop, group + j) << (8 * j);
           keep[i] = transpose_bits(word, lane);
         }

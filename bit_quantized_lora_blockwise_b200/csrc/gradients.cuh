@@ -1,0 +1,311 @@
+// Adapter gradients of many experts in one persistent launch:
+//   dA_e = (M o X_e)^T Gs_e   [K, r],      dB_e = s (XA_e^T dY_e)   [r, N]
+// (M: the dropout mask, 1 without dropout), each the product over the
+// expert's tokens alone. skinny_kernel computes the same sums with one
+// cluster per tile, split over the tokens; with more tiles than resident CTAs
+// its cost is the CTA itself (tables, TMEM, first copies, shared-memory
+// reduction: some 10 us), not the sums. Here two CTAs per SM run over the
+// (product, expert, 128-row tile) units with the ring running on from one unit
+// to the next and two TMEM accumulators, so that a unit's readout overlaps the
+// next one's products. Bound by reading X and dY once.
+//
+// The token rows are the MMA's K: MN-major operands, 64 tokens a stage, from
+// the expert's first row on (a row coordinate, aligned to nothing). The last
+// block may reach into the next expert's rows: warp 2 sets those rows of both
+// operands to zero in shared memory before the MMAs read them, so not even a
+// NaN there can enter. An expert without tokens gets zeros.
+//
+// Roles: warp 0 TMA, warp 1 TMEM + MMA, warp 2 tails, warps 4-7 readout and
+// stores, warps 8-15 (DROP) take each landed stage of X through the mask.
+#pragma once
+
+#include "dropout.cuh"
+#include "groups.cuh"
+#include "ptx.cuh"
+
+namespace qlora {
+
+struct GradientArgs {
+  CUtensorMap tm_x, tm_gs;   // X [T, K], Gs [T, r]: 64 x 64 boxes
+  CUtensorMap tm_dy, tm_xa;  // dY [T, N], XA [T, r]
+  void *dA, *dB;             // [E, K, r], [E, r, N], 16-bit
+  float b_scale;             // s
+  int K, N, r;
+  int f16;
+  GroupArgs groups;
+  DropoutArgs drop;
+};
+
+template <int BN_, int STAGES_, bool DROP_>
+struct GradientCfg {
+  static constexpr int BN = BN_, STAGES = STAGES_;
+  static constexpr bool DROP = DROP_;
+  static constexpr int A_BYTES = 128 * 64 * 2, B_BYTES = BN_ * 64 * 2, STAGE = A_BYTES + B_BYTES;
+  static constexpr int OFF_BAR = STAGES_ * STAGE;
+  // full[S] empty[S] ready[S] tmem_full[2] tmem_empty[2] landed tail drain
+  static constexpr int NBARS = 3 * STAGES_ + 7;
+  static constexpr int OFF_MISC = (OFF_BAR + NBARS * 8 + 15) & ~15;
+  static constexpr int OFF_GROUPS = OFF_MISC + 16;
+  static constexpr int SMEM_BYTES = OFF_GROUPS + kGroupTableBytes;
+  static constexpr int THREADS = DROP_ ? 512 : 256;
+  static constexpr uint32_t TMEM_COLS = 2 * BN_;
+  static constexpr int PER_SM = SMEM_BYTES <= 113 * 1024 ? 2 : 1;
+  static_assert(BN_ == 64 || BN_ == 128 || BN_ == 256, "rank tile");
+  static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const __grid_constant__ GradientArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bar0 = sbase + C::OFF_BAR;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (C::STAGES + s); };
+  auto ready_bar = [&](int s) { return bar0 + 8u * (2 * C::STAGES + s); };
+  auto tmem_full = [&](int b) { return bar0 + 8u * (3 * C::STAGES + b); };
+  auto tmem_empty = [&](int b) { return bar0 + 8u * (3 * C::STAGES + 2 + b); };
+  const uint32_t landed_bar = bar0 + 8u * (3 * C::STAGES + 4), tail_bar = landed_bar + 8u, drain_bar = tail_bar + 8u;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
+  volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+  const GroupTable gt = group_table(smem + C::OFF_GROUPS);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+      mbar_init(ready_bar(s), 8);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tmem_full(b), 1);
+      mbar_init(tmem_empty(b), 4);
+    }
+    mbar_init(landed_bar, 1);
+    mbar_init(tail_bar, 1);
+    mbar_init(drain_bar, 1);
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(s_tmem), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  // Late, like the dense backward's last launch: every operand is complete
+  // when this launch starts, and nothing it writes is touched by the kernel
+  // before it, for which each thread waits only before exiting.
+  grid_dep_launch();
+  if (warp == 3) build_group_table(a.groups, 64, gt);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+
+  const int ta = (a.K + 127) / 128, tb = (a.N + 127) / 128;
+  const int na = a.groups.groups * ta, units = na + a.groups.groups * tb;
+  struct Unit {
+    bool second;  // dB
+    int group, row0, tok0, ntok, nk;
+  };
+  auto unit_at = [&](int u) {
+    Unit t;
+    t.second = u >= na;
+    const int v = t.second ? u - na : u, per = t.second ? tb : ta;
+    t.group = v / per;
+    t.row0 = (v - t.group * per) * 128;
+    t.tok0 = gt.first[t.group];
+    t.ntok = gt.first[t.group + 1] - t.tok0;
+    t.nk = (t.ntok + 63) / 64;
+    return t;
+  };
+
+  if (warp == 0) {
+    if (elect_one()) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        const Unit t = unit_at(u);
+        const CUtensorMap *ma = t.second ? &a.tm_dy : &a.tm_x, *mb = t.second ? &a.tm_xa : &a.tm_gs;
+        for (int j = 0; j < t.nk; ++j, ++it) {
+          const int s = it % C::STAGES, tok = t.tok0 + j * 64;
+          if (!mbar_wait(empty_bar(s), ((it / C::STAGES) & 1u) ^ 1u, s_abort)) { ok = false; break; }
+          const uint32_t dst = sbase + s * C::STAGE;
+          mbar_arrive_expect_tx(full_bar(s), C::STAGE);
+          tma_load_2d(dst, ma, full_bar(s), t.row0, tok);
+          tma_load_2d(dst + 8192, ma, full_bar(s), t.row0 + 64, tok);
+#pragma unroll
+          for (int c = 0; c < C::BN / 64; ++c) tma_load_2d(dst + C::A_BYTES + c * 8192, mb, full_bar(s), c * 64, tok);
+        }
+      }
+      // wait (bounded) for the copies still in flight
+      const uint32_t inflight = it < static_cast<uint32_t>(C::STAGES) ? it : C::STAGES;
+      for (uint32_t i = 0; i < inflight; ++i) {
+        const uint32_t jb = it - 1 - i;
+        const unsigned long long t0 = globaltimer_ns();
+        while (!mbar_try_wait(full_bar(jb % C::STAGES), (jb / C::STAGES) & 1u)) {
+          if (globaltimer_ns() - t0 > kWaitTimeoutNs) break;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (elect_one()) {
+      const uint32_t idesc = idesc_dtype(make_idesc_bf16(128, C::BN, 1, 1), a.f16);
+      uint32_t it = 0, use = 0, tails = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        const Unit t = unit_at(u);
+        if (t.nk == 0) continue;
+        const int b = use & 1u;
+        if (!mbar_wait(tmem_empty(b), ((use >> 1) & 1u) ^ 1u, s_abort)) { ok = false; break; }
+        tc_fence_after();
+        for (int j = 0; j < t.nk; ++j, ++it) {
+          const int s = it % C::STAGES;
+          if (!mbar_wait(C::DROP ? ready_bar(s) : full_bar(s), (it / C::STAGES) & 1u, s_abort)) { ok = false; break; }
+          if (j == t.nk - 1 && (t.ntok & 63)) {  // (only this thread follows the ring's phases)
+            mbar_arrive(landed_bar);
+            if (!mbar_wait(tail_bar, tails & 1u, s_abort)) { ok = false; break; }
+            ++tails;
+          }
+          tc_fence_after();
+          const uint32_t ad = sbase + s * C::STAGE, bd = ad + C::A_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_ss(tmem_base + b * C::BN, smem_desc_sw128(ad + kk * 2048, 8192, 1024),
+                      smem_desc_sw128(bd + kk * 2048, 8192, 1024), idesc, (j > 0 || kk > 0) ? 1u : 0u);
+          tc_commit(empty_bar(s));
+        }
+        if (!ok) break;
+        tc_commit(tmem_full(b));
+        ++use;
+      }
+      if (it > 0) {
+        tc_commit(drain_bar);
+        const unsigned long long t0 = globaltimer_ns();
+        while (!mbar_try_wait(drain_bar, 0)) {
+          if (globaltimer_ns() - t0 > kWaitTimeoutNs) break;
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    uint32_t it = 0, tails = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+      const Unit t = unit_at(u);
+      it += t.nk;
+      const int rows = t.ntok & 63;
+      if (rows == 0) continue;
+      // once the last block has landed (and X is masked): its rows past the
+      // expert's last token (a row is 128 consecutive bytes of each 64 x 64
+      // chunk, whatever the swizzle)
+      if (!warp_wait_all(landed_bar, tails & 1u, s_abort)) break;
+      ++tails;
+      uint8_t *stage = smem + (it - 1) % C::STAGES * C::STAGE;
+      const int first = rows * 8, per = 512 - first;  // 16-byte pieces of a chunk
+      for (int i = lane; i < per * (2 + C::BN / 64); i += 32) {
+        const int c = i / per, o = first + i - c * per;
+        *reinterpret_cast<uint4 *>(stage + c * 8192 + o * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tail_bar);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    const int q = warp - 4;
+    const bool f16 = a.f16 != 0;
+    uint32_t use = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+      const Unit t = unit_at(u);
+      const int b = use & 1u;
+      if (t.nk > 0) {
+        if (!warp_wait_all(tmem_full(b), (use >> 1) & 1u, s_abort)) break;
+        tc_fence_after();
+      }
+      const int base = t.row0 + q * 32;  // K and N are multiples of 64: 32 rows or none
+#pragma unroll 1
+      for (int c0 = 0; c0 < a.r && base < (t.second ? a.N : a.K); c0 += 32) {
+        float v[32];
+        if (t.nk > 0) {
+          uint32_t w[32];
+          tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * C::BN + c0, w);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]) * (t.second ? a.b_scale : 1.0f);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+        }
+        if (!t.second) {  // a row of dA per lane
+          uint16_t *dst = reinterpret_cast<uint16_t *>(a.dA) +
+                          (static_cast<int64_t>(t.group) * a.K + base + lane) * a.r + c0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c0 + 8 * i < a.r)
+              *reinterpret_cast<uint4 *>(dst + 8 * i) =
+                  make_uint4(pack_16x2(v[8 * i], v[8 * i + 1], f16), pack_16x2(v[8 * i + 2], v[8 * i + 3], f16),
+                             pack_16x2(v[8 * i + 4], v[8 * i + 5], f16), pack_16x2(v[8 * i + 6], v[8 * i + 7], f16));
+        } else {  // dB is stored along N
+          uint4 out[4];
+          rows_to_columns(v, lane, f16, out);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int col = c0 + 8 * i + (lane & 7);
+            if (col < a.r)
+              *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.dB) +
+                                         (static_cast<int64_t>(t.group) * a.r + col) * a.N + base + (lane >> 3) * 8) =
+                  out[i];
+          }
+        }
+      }
+      if (t.nk > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tmem_empty(b));
+        ++use;
+      }
+    }
+  } else if (C::DROP && warp >= 8) {
+    // M o X. 16-byte piece c of row r of a 64-wide chunk lies at c ^ (r & 7)
+    // in the row's 128 bytes; a thread's four pieces are 32 rows apart, their
+    // masks formed side by side before the stage is waited for. (Rows past
+    // the expert's last token are masked too, and then zeroed.)
+    const int tid = (warp - 8) * 32 + lane, c = tid & 7, r0 = tid >> 3;
+    const uint32_t swz = static_cast<uint32_t>(c ^ (r0 & 7)) << 4;
+    const uint64_t ld8 = static_cast<uint64_t>(a.K) / 8;
+    uint32_t it = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      const Unit t = unit_at(u);
+      for (int j = 0; j < t.nk; ++j, ++it) {
+        const int s = it % C::STAGES;
+        uint4 mask[4];
+        if (!t.second) {
+          const uint64_t first = static_cast<uint64_t>(t.tok0 + j * 64 + r0) * ld8 + (t.row0 / 8 + c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mask[i] = dropout_mask8(a.drop, first + (i & 1) * 32 * ld8 + (i >> 1) * 8);
+        }
+        if (!warp_wait_all(full_bar(s), (it / C::STAGES) & 1u, s_abort)) { ok = false; break; }
+        if (!t.second) {
+          uint8_t *piece = smem + s * C::STAGE + r0 * 128 + swz;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 *at = reinterpret_cast<uint4 *>(piece + i * 4096);
+            const uint4 v = *at;
+            *at = make_uint4(v.x & mask[i].x, v.y & mask[i].y, v.z & mask[i].z, v.w & mask[i].w);
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ready_bar(s));
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+  grid_dep_wait();
+}
+
+}  // namespace qlora

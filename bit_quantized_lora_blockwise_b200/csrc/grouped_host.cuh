@@ -102,15 +102,12 @@ qlora_status check_grouped(const GroupedShape &s) {
 // Threshold and factor of a dropout description (dropout.cuh); NULL or a
 // threshold of 0 drops nothing.
 qlora_status make_dropout(const qlora_dropout_desc *d, DropoutArgs *out) {
-  *out = DropoutArgs{0, 0, 0u, 1.0f};
+  *out = dropout_args(0, 0, 0u);
   if (d == nullptr) return QLORA_OK;
   if (!(d->p >= 0.0 && d->p < 1.0)) return QLORA_ERR_RANGE;
   const double t = std::floor(d->p * 65536.0 + 0.5);
   if (t > 65535.0) return QLORA_ERR_RANGE;
-  out->seed = d->seed;
-  out->offset = d->offset;
-  out->threshold = static_cast<uint32_t>(t);
-  out->factor = static_cast<float>(65536.0 / (65536.0 - t));
+  *out = dropout_args(d->seed, d->offset, static_cast<uint32_t>(t));
   return QLORA_OK;
 }
 
@@ -184,11 +181,56 @@ qlora_status grouped_rows(SkinnyKind kind, const void *rows, const void *adapter
                        : run_skinny<false, false, true>(a, p.bn, grid, st);
 }
 
-// dA_e = (M o X_e)^T gs_e and dB_e = s xa_e^T dY_e, every expert's in one launch.
+template <int BN, bool DROP>
+qlora_status run_gradients_bn(const GradientArgs &a, int64_t units, int sms, cudaStream_t st) {
+  using C = GradientCfg<BN, skinny_stages(BN), DROP>;
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t err[kMaxDevices];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::call_once(once[dev], [&] {
+    err[dev] = cudaFuncSetAttribute(gradient_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (err[dev] == cudaSuccess)
+      err[dev] = cudaFuncSetAttribute(gradient_kernel<C>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                      static_cast<int>(cudaSharedmemCarveoutMaxShared));
+  });
+  if (err[dev] != cudaSuccess) return QLORA_ERR_CUDA;
+  const int grid = static_cast<int>(std::min<int64_t>(units, static_cast<int64_t>(C::PER_SM) * sms));
+  return launch_pdl(gradient_kernel<C>, grid, C::THREADS, C::SMEM_BYTES, st, a);
+}
+
+template <bool DROP>
+qlora_status run_gradients(const GradientArgs &a, int64_t units, int sms, cudaStream_t st) {
+  const int bn = rank_tile(a.r);
+  if (bn == 64) return run_gradients_bn<64, DROP>(a, units, sms, st);
+  if (bn == 128) return run_gradients_bn<128, DROP>(a, units, sms, st);
+  return run_gradients_bn<256, DROP>(a, units, sms, st);
+}
+
+// dA_e = (M o X_e)^T gs_e and dB_e = s xa_e^T dY_e, every expert's in one
+// launch: over persistent CTAs when there are more 128-row tiles than CTAs
+// that can be resident, else with each tile's tokens split over a cluster.
 qlora_status grouped_adapter_grads(const void *X, const void *dY, const void *gs, const void *xa, const GroupedShape &s,
                                    const GroupArgs &g, const DropoutArgs &drop, void *dA, void *dB, float b_scale,
-                                   cudaStream_t st) {
+                                   int sms, cudaStream_t st) {
   const int64_t ta = s.E * cdiv(s.K, 128), tb = s.E * cdiv(s.N, 128);
+  if (ta + tb > (s.r <= 128 ? 2 : 1) * static_cast<int64_t>(sms)) {
+    GradientArgs a;
+    std::memset(&a, 0, sizeof a);
+    if (!map_mnmajor(&a.tm_x, X, s.K, s.T) || !map_mnmajor(&a.tm_gs, gs, s.r, s.T) ||
+        !map_mnmajor(&a.tm_dy, dY, s.N, s.T) || !map_mnmajor(&a.tm_xa, xa, s.r, s.T))
+      return QLORA_ERR_CUDA;
+    a.dA = dA;
+    a.dB = dB;
+    a.b_scale = b_scale;
+    a.K = static_cast<int>(s.K);
+    a.N = static_cast<int>(s.N);
+    a.r = s.r;
+    a.f16 = t_f16 ? 1 : 0;
+    a.groups = g;
+    a.drop = drop;
+    return s.drop ? run_gradients<true>(a, ta + tb, sms, st) : run_gradients<false>(a, ta + tb, sms, st);
+  }
   SkinnyPlan p;
   const qlora_status e = s.drop ? plan_skinny_v<true, true, true, true>((ta + tb) * 128, cdiv(s.T, s.E), s.r, &p)
                                 : plan_skinny_v<true, true, true>((ta + tb) * 128, cdiv(s.T, s.E), s.r, &p);
@@ -349,5 +391,5 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
 
   // 3) dA and dB "late", as in the dense backward: every operand is complete
   //    when this launch starts and dX is neither read nor written by it
-  return grouped_adapter_grads(X, dY, gs, XA, s, g, drop, dA, dB, scl, cs);
+  return grouped_adapter_grads(X, dY, gs, XA, s, g, drop, dA, dB, scl, sms, cs);
 }

@@ -22,6 +22,7 @@
 #include "skinny.cuh"
 #include "smallm.cuh"
 #include "dropout.cuh"
+#include "gradients.cuh"
 #include "groups.cuh"
 #include "adamw.cuh"
 #include "ptx.cuh"

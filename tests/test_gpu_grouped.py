@@ -173,6 +173,19 @@ def test_many_experts():
     check(Layer(np.bincount(rng.integers(0, 40, 2500), minlength=40), 128, 128, 8, seed=10))
 
 
+@pytest.mark.parametrize("r,dt,p", [(8, BF, 0.0), (64, HF, 0.1), (72, BF, 0.5), (128, BF, 0.0), (136, HF, 0.0),
+                                    (256, BF, 0.1)])
+def test_more_tiles_than_resident_ctas(r, dt, p):
+    """Enough experts and rows that the adapter gradients run over persistent CTAs, several units each: empty experts,
+    whole and ragged 64-token blocks, experts that start anywhere."""
+    counts = [0, 1, 64, 130, 0, 63, 65, 200, 5, 128, 0, 17] * 3
+    drop = binding.Dropout(p, 9, 1) if p else None
+    L = Layer(counts, 704, 576, r, dt, seed=r, lead=5, trail=9, std=0.02)  # 36 x (5 + 6) = 396 tiles of 128 rows
+    first = check(L, drop)
+    again = L.bwd(first[1], drop)
+    assert all(torch.equal(x, y) for x, y in zip(first[2:], again))
+
+
 @pytest.mark.parametrize("drop", [None, binding.Dropout(0.2, 3)])
 @pytest.mark.parametrize("T", [1, 20, 33, 300, 1100])
 def test_one_expert_without_offsets_is_the_dense_linear(T, drop):
