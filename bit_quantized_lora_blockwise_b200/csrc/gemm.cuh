@@ -25,11 +25,11 @@
 // peer's producers and epilogue arrive on the leader's barriers remotely; the
 // leader's commits release the stages and accumulators of both CTAs.
 //
-// Token stages. On this part a TMA load costs about the same time whether it
-// moves 16 KB or 64 KB, so one B stage holds BKB consecutive 64-deep K blocks
-// of the CTA's tokens, fetched by one 3-D box (the token operand viewed as
-// {64, tokens, K/64}); the MMAs of BKB jobs read it before it is released.
-// Low-rank K blocks take one B stage each (two 2-D boxes: B2 and A2).
+// Token stages. A B stage holds BKB consecutive 64-deep K blocks of the CTA's
+// tokens, fetched by one 3-D box (the token operand viewed as {64, tokens,
+// K/64}); the MMAs of BKB jobs read it before it is released. Low-rank K
+// blocks take one B stage each (two 2-D boxes: B2 and A2). The pairs hold one
+// K block per stage and share the stage with the decoded weights (ONE_RING).
 //
 // Token sub-tiles (NTT). Every 64-deep job has fixed costs (a decoded tile
 // handed from the producers to the MMA thread, a stage released, barrier
@@ -49,8 +49,9 @@
 //   warp 5     TMEM allocation + MMA issue (one lane of the leader)
 //   warp 6     TMA issue for the packed-code ring (one lane)
 //   warps 7..  dequant producers (NPW warps, in groups of 4 that take turns)
-// Rings (mbarrier-guarded): B (SB stages), dequantized A (SA stages, one per
-// 64-deep job), packed codes (SP slots of KSUP jobs; each producer thread
+// Rings (mbarrier-guarded): B (SB stages) and dequantized A (SA stages, one per
+// 64-deep job), one ring for both in pairs; packed codes (SP slots of KSUP
+// jobs; each producer thread
 // reads its block's 8-bit constant code and second-level scale from global
 // memory one job ahead); two TMEM accumulators (tmem_full, tmem_empty) so the
 // epilogue of one tile overlaps the mainloop of the next. Every wait is bounded (mbar_wait); on a

@@ -87,6 +87,8 @@ GroupedWs grouped_ws(const GroupedShape &s, int64_t ncounters, size_t part, bool
   return w;
 }
 
+static_assert(QLORA_MAX_EXPERTS == kMaxGroups, "the group table holds every expert");
+
 // Shapes that every grouped kernel can index: weight rows, tile and unit
 // counts stay within int32.
 qlora_status check_grouped(const GroupedShape &s) {
@@ -267,7 +269,7 @@ qlora_status grouped_adapter_grads(const void *X, const void *dY, const void *gs
 
 template <class C>
 qlora_status run_grouped_gemm(const GemmArgs &args, int slots, cudaStream_t stream) {
-  if (slots < 1) return QLORA_ERR_CUDA;  // (resident_pairs has set the kernel's shared memory)
+  // (resident_pairs has set the kernel's shared memory)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * slots);
   cfg.blockDim = dim3(C::THREADS);
@@ -316,6 +318,7 @@ qlora_status grouped_fwd(const uint8_t *packed, const uint8_t *q, const float *s
   const GroupedPlanHost p = plan_grouped_host(s, s.K / 64, sms);
   const GroupedWs w = grouped_ws(s, p.counters, p.part, false);
   if (!workspace || workspace_bytes < w.total) return QLORA_ERR_WORKSPACE;
+  if (p.slots < 1) return QLORA_ERR_CUDA;  // no room for a CTA pair
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   unsigned int *counters = reinterpret_cast<unsigned int *>(ws);
   void *xas = ws + w.counters;
@@ -351,6 +354,7 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
   const GroupedPlanHost p = plan_grouped_host(s, s.N / 64, sms);
   const GroupedWs w = grouped_ws(s, p.counters, p.part, true);
   if (!workspace || workspace_bytes < w.total) return QLORA_ERR_WORKSPACE;
+  if (p.slots < 1) return QLORA_ERR_CUDA;  // no room for a CTA pair
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   unsigned int *counters = reinterpret_cast<unsigned int *>(ws);
   void *gs = ws + w.counters;

@@ -38,13 +38,19 @@ __device__ __forceinline__ GroupTable group_table(uint8_t *smem) {
 // them, bit 1 of the device error word is set.
 __device__ __forceinline__ void build_group_table(const GroupArgs &a, int tile, const GroupTable &t) {
   const int lane = threadIdx.x & 31;
+  // all the loads first: a scan that waited for each 32 offsets in turn would
+  // cost a trip to L2 per 32 experts
+#pragma unroll 8
+  for (int i = lane; i <= a.groups; i += 32)
+    t.first[i] = a.offsets != nullptr ? __ldg(a.offsets + i) : (i == 0 ? 0 : a.tokens);
+  __syncwarp();
   int carry = 0;
   bool bad = false;
   for (int base = 0; base <= a.groups; base += 32) {
     const int i = base + lane;
     int v = 0;
     if (i <= a.groups) {
-      const int raw = a.offsets != nullptr ? __ldg(a.offsets + i) : (i == 0 ? 0 : a.tokens);
+      const int raw = t.first[i];
       v = raw < 0 ? 0 : (raw > a.tokens ? a.tokens : raw);
       bad |= v != raw;
     }
