@@ -126,8 +126,8 @@ def check(L, drop=None, save_xa=True):
     return Y, XA, dX, dA, dB
 
 
-# counts per expert and the path that the average picks: the register stream (up to 24 tokens an expert), one and two
-# 256-token sub-tiles; each with experts without tokens, ragged tails and uneven experts
+# counts per expert, on both sides of the average that picks one or two 256-token sub-tiles; each with experts without
+# tokens, ragged tails and uneven experts
 COUNTS = [[1], [0, 1], [2, 0, 0, 3], [8, 9, 16, 17, 0, 33], [0, 0, 64], [32, 65, 0, 1], [25], [100, 0, 64, 63], [256, 257],
           [300, 1, 0, 129], [384], [512, 513], [1025, 0, 700], [1, 1400]]
 
