@@ -126,6 +126,7 @@ struct GemmArgs {
   GroupArgs groups;
   int expert_rows;    // N: weight rows of one expert
   DropoutArgs drop;   // DROP: the adapter dropout of dX, over [tokens, rows] (its factor is in B2)
+  uint32_t *keep_bits;  // DROP, optional: the keep bits it evaluates, [tokens][rows / 32], for dA
 };
 
 template <int BN_, int ASRC_, int L2_, int BKB_, int SB_, int SA_, int SP_, int NPW_, bool PAIR_, int NTT_ = 1,
@@ -752,6 +753,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
           uint32_t word = 0u;
 #pragma unroll
           for (int j = 0; j < 4; ++j) word |= dropout_keep8(args.drop, group + j) << (8 * j);
+          if (args.keep_bits != nullptr && tok < end) args.keep_bits[group / 4] = word;
           keep[i] = transpose_bits(word, lane);
         }
         return;

@@ -15,11 +15,17 @@
 // operands to zero in shared memory before the MMAs read them, so not even a
 // NaN there can enter. An expert without tokens gets zeros.
 //
+// Dropout: dX, the launch before this one, evaluates the same mask and leaves
+// its keep bits in the workspace (T K / 8 bytes; evaluated here once more, the
+// generator's integer work took 93 us where reading takes @T@: 8192 rows, 8
+// experts of 4096 x 11008). The units of dB come first: they need nothing from
+// dX and fill the SMs that its last round leaves idle; every role waits for dX
+// before its first unit of dA.
+//
 // Roles: warp 0 TMA, warp 1 TMEM + MMA, warp 2 tails, warps 4-7 readout and
 // stores, warps 8-15 (DROP) take each landed stage of X through the mask.
 #pragma once
 
-#include "dropout.cuh"
 #include "groups.cuh"
 #include "ptx.cuh"
 
@@ -33,7 +39,7 @@ struct GradientArgs {
   int K, N, r;
   int f16;
   GroupArgs groups;
-  DropoutArgs drop;
+  const uint32_t *keep;  // DROP: keep bits of X, [T][K / 32], written by the kernel before this one
 };
 
 template <int BN_, int STAGES_, bool DROP_>
@@ -101,15 +107,15 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
   const uint32_t tmem_base = *s_tmem;
 
   const int ta = (a.K + 127) / 128, tb = (a.N + 127) / 128;
-  const int na = a.groups.groups * ta, units = na + a.groups.groups * tb;
+  const int nb = a.groups.groups * tb, units = nb + a.groups.groups * ta;
   struct Unit {
     bool second;  // dB
     int group, row0, tok0, ntok, nk;
   };
   auto unit_at = [&](int u) {
     Unit t;
-    t.second = u >= na;
-    const int v = t.second ? u - na : u, per = t.second ? tb : ta;
+    t.second = u < nb;
+    const int v = t.second ? u : u - nb, per = t.second ? tb : ta;
     t.group = v / per;
     t.row0 = (v - t.group * per) * 128;
     t.tok0 = gt.first[t.group];
@@ -118,12 +124,22 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
     return t;
   };
 
+  // (each thread of a role, unit by unit; the bounded waits start after it)
+  bool dx_done = !C::DROP;
+  auto wait_dx = [&](const Unit &t) {
+    if (!dx_done && !t.second) {
+      grid_dep_wait();
+      dx_done = true;
+    }
+  };
+
   if (warp == 0) {
     if (elect_one()) {
       uint32_t it = 0;
       bool ok = true;
       for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const Unit t = unit_at(u);
+        wait_dx(t);
         const CUtensorMap *ma = t.second ? &a.tm_dy : &a.tm_x, *mb = t.second ? &a.tm_xa : &a.tm_gs;
         for (int j = 0; j < t.nk; ++j, ++it) {
           const int s = it % C::STAGES, tok = t.tok0 + j * 64;
@@ -154,6 +170,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
       bool ok = true;
       for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const Unit t = unit_at(u);
+        wait_dx(t);
         if (t.nk == 0) continue;
         const int b = use & 1u;
         if (!mbar_wait(tmem_empty(b), ((use >> 1) & 1u) ^ 1u, s_abort)) { ok = false; break; }
@@ -191,6 +208,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
     uint32_t it = 0, tails = 0;
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
       const Unit t = unit_at(u);
+      wait_dx(t);
       it += t.nk;
       const int rows = t.ntok & 63;
       if (rows == 0) continue;
@@ -216,6 +234,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
       const Unit t = unit_at(u);
       const int b = use & 1u;
+      wait_dx(t);
       if (t.nk > 0) {
         if (!warp_wait_all(tmem_full(b), (use >> 1) & 1u, s_abort)) break;
         tc_fence_after();
@@ -264,32 +283,34 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
     }
   } else if (C::DROP && warp >= 8) {
     // M o X. 16-byte piece c of row r of a 64-wide chunk lies at c ^ (r & 7)
-    // in the row's 128 bytes; a thread's four pieces are 32 rows apart, their
-    // masks formed side by side before the stage is waited for. (Rows past
-    // the expert's last token are masked too, and then zeroed.)
-    const int tid = (warp - 8) * 32 + lane, c = tid & 7, r0 = tid >> 3;
-    const uint32_t swz = static_cast<uint32_t>(c ^ (r0 & 7)) << 4;
-    const uint64_t ld8 = static_cast<uint64_t>(a.K) / 8;
+    // in the row's 128 bytes. A thread takes 32 columns of a token row, one
+    // word of keep bits and four pieces of one chunk; 8 lanes' rows differ, so
+    // the pieces they touch at a time lie in different banks. Bit 8 i + 7 - k
+    // of the word shifted left by k is the sign of byte i, which prmt spreads
+    // over a 16-bit element. (Rows past the expert's last token are not
+    // masked: warp 2 zeroes them.)
+    const int r = (warp - 8) * 8 + (lane & 7), word = lane >> 3;
+    const int64_t ld = a.K / 32;
     uint32_t it = 0;
     bool ok = true;
     for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
       const Unit t = unit_at(u);
+      wait_dx(t);
+      const uint32_t *bits = a.keep + static_cast<int64_t>(t.tok0 + r) * ld + t.row0 / 32 + word;
+      const bool in_row = t.row0 / 32 + word < ld;
       for (int j = 0; j < t.nk; ++j, ++it) {
         const int s = it % C::STAGES;
-        uint4 mask[4];
-        if (!t.second) {
-          const uint64_t first = static_cast<uint64_t>(t.tok0 + j * 64 + r0) * ld8 + (t.row0 / 8 + c);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mask[i] = dropout_mask8(a.drop, first + (i & 1) * 32 * ld8 + (i >> 1) * 8);
-        }
+        const uint32_t w = !t.second && in_row && j * 64 + r < t.ntok ? __ldcg(bits + j * 64 * ld) : 0u;
         if (!warp_wait_all(full_bar(s), (it / C::STAGES) & 1u, s_abort)) { ok = false; break; }
         if (!t.second) {
-          uint8_t *piece = smem + s * C::STAGE + r0 * 128 + swz;
+          uint8_t *row = smem + s * C::STAGE + (word >> 1) * 8192 + r * 128;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint4 *at = reinterpret_cast<uint4 *>(piece + i * 4096);
+            uint4 *at = reinterpret_cast<uint4 *>(row + ((((word & 1) * 4 + i) ^ (r & 7)) << 4));
+            const uint32_t sel = 0x0101u * (0x88u + 0x11u * i) + 0x4400u;  // byte i of both sources, signs only
             const uint4 v = *at;
-            *at = make_uint4(v.x & mask[i].x, v.y & mask[i].y, v.z & mask[i].z, v.w & mask[i].w);
+            *at = make_uint4(v.x & prmt(w << 7, w << 6, sel), v.y & prmt(w << 5, w << 4, sel),
+                             v.z & prmt(w << 3, w << 2, sel), v.w & prmt(w << 1, w, sel));
           }
           fence_proxy_async_smem();
         }

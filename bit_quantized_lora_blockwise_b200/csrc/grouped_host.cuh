@@ -74,16 +74,24 @@ GroupedPlanHost plan_grouped_host(const GroupedShape &s, int64_t kblocks, int sm
   return p;
 }
 
-// [counters][16-bit T x r][16-bit T x r (backward)][fp32 partials]
+// dA and dB over persistent CTAs (gradient_kernel): when there are more 128-row
+// tiles than CTAs that can be resident.
+bool persistent_gradients(const GroupedShape &s, int sms) {
+  return s.E * (cdiv(s.K, 128) + cdiv(s.N, 128)) > (s.r <= 128 ? 2 : 1) * static_cast<int64_t>(sms);
+}
+
+// [counters][16-bit T x r][16-bit T x r (backward)][fp32 partials][keep bits T x
+// K / 8 (backward with dropout, for gradient_kernel)]
 struct GroupedWs {
-  size_t counters, tr, part, total;
+  size_t counters, tr, part, keep, total;
 };
-GroupedWs grouped_ws(const GroupedShape &s, int64_t ncounters, size_t part, bool backward) {
+GroupedWs grouped_ws(const GroupedShape &s, int64_t ncounters, size_t part, bool backward, int sms) {
   GroupedWs w;
   w.counters = align256(static_cast<size_t>(ncounters) * 4);
   w.tr = align256(static_cast<size_t>(s.T) * s.r * 2);
   w.part = part;
-  w.total = w.counters + (backward ? 2 : 1) * w.tr + w.part;
+  w.keep = backward && s.drop && persistent_gradients(s, sms) ? align256(static_cast<size_t>(s.T) * (s.K / 8)) : 0;
+  w.total = w.counters + (backward ? 2 : 1) * w.tr + w.part + w.keep;
   return w;
 }
 
@@ -210,13 +218,13 @@ qlora_status run_gradients(const GradientArgs &a, int64_t units, int sms, cudaSt
 }
 
 // dA_e = (M o X_e)^T gs_e and dB_e = s xa_e^T dY_e, every expert's in one
-// launch: over persistent CTAs when there are more 128-row tiles than CTAs
-// that can be resident, else with each tile's tokens split over a cluster.
+// launch: over persistent CTAs (`keep`: the mask's bits, which dX left), else
+// with each tile's tokens split over a cluster.
 qlora_status grouped_adapter_grads(const void *X, const void *dY, const void *gs, const void *xa, const GroupedShape &s,
-                                   const GroupArgs &g, const DropoutArgs &drop, void *dA, void *dB, float b_scale,
-                                   int sms, cudaStream_t st) {
+                                   const GroupArgs &g, const DropoutArgs &drop, const uint32_t *keep, void *dA,
+                                   void *dB, float b_scale, int sms, cudaStream_t st) {
   const int64_t ta = s.E * cdiv(s.K, 128), tb = s.E * cdiv(s.N, 128);
-  if (ta + tb > (s.r <= 128 ? 2 : 1) * static_cast<int64_t>(sms)) {
+  if (persistent_gradients(s, sms)) {
     GradientArgs a;
     std::memset(&a, 0, sizeof a);
     if (!map_mnmajor(&a.tm_x, X, s.K, s.T) || !map_mnmajor(&a.tm_gs, gs, s.r, s.T) ||
@@ -230,7 +238,7 @@ qlora_status grouped_adapter_grads(const void *X, const void *dY, const void *gs
     a.r = s.r;
     a.f16 = t_f16 ? 1 : 0;
     a.groups = g;
-    a.drop = drop;
+    a.keep = keep;
     return s.drop ? run_gradients<true>(a, ta + tb, sms, st) : run_gradients<false>(a, ta + tb, sms, st);
   }
   SkinnyPlan p;
@@ -316,7 +324,7 @@ qlora_status grouped_fwd(const uint8_t *packed, const uint8_t *q, const float *s
                          const void *B, float alpha, const DropoutArgs &drop, void *Y, void *XA_out, void *workspace,
                          size_t workspace_bytes, int sms, cudaStream_t cs) {
   const GroupedPlanHost p = plan_grouped_host(s, s.K / 64, sms);
-  const GroupedWs w = grouped_ws(s, p.counters, p.part, false);
+  const GroupedWs w = grouped_ws(s, p.counters, p.part, false, sms);
   if (!workspace || workspace_bytes < w.total) return QLORA_ERR_WORKSPACE;
   if (p.slots < 1) return QLORA_ERR_CUDA;  // no room for a CTA pair
   uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -352,7 +360,7 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
                          const void *A, const void *B, const void *XA, float alpha, const DropoutArgs &drop, void *dX,
                          void *dA, void *dB, void *workspace, size_t workspace_bytes, int sms, cudaStream_t cs) {
   const GroupedPlanHost p = plan_grouped_host(s, s.N / 64, sms);
-  const GroupedWs w = grouped_ws(s, p.counters, p.part, true);
+  const GroupedWs w = grouped_ws(s, p.counters, p.part, true, sms);
   if (!workspace || workspace_bytes < w.total) return QLORA_ERR_WORKSPACE;
   if (p.slots < 1) return QLORA_ERR_CUDA;  // no room for a CTA pair
   uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -360,6 +368,7 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
   void *gs = ws + w.counters;
   void *xa_ws = ws + w.counters + w.tr;
   float *part = reinterpret_cast<float *>(ws + w.counters + 2 * w.tr);
+  uint32_t *keep = w.keep > 0 ? reinterpret_cast<uint32_t *>(ws + w.counters + 2 * w.tr + w.part) : nullptr;
   const GroupArgs g{offsets, static_cast<int>(s.E), static_cast<int>(s.T)};
   const float scl = alpha / static_cast<float>(s.r);
   qlora_status st = QLORA_OK;
@@ -385,6 +394,7 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
     return QLORA_ERR_CUDA;
   grouped_gemm_args(&a, q, scale2, nf4, t8, s, g, s.K, s.N / 64, dX, part, counters);
   a.drop = drop;
+  a.keep_bits = keep;
   trace_begin(cs);
   if (s.drop)
     st = p.ntt == 2 ? run_grouped_gemm<GroupedBwdDrop2>(a, p.slots, cs) : run_grouped_gemm<GroupedBwdDrop1>(a, p.slots, cs);
@@ -393,7 +403,8 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
   trace_end(cs);
   if (st != QLORA_OK) return st;
 
-  // 3) dA and dB "late", as in the dense backward: every operand is complete
-  //    when this launch starts and dX is neither read nor written by it
-  return grouped_adapter_grads(X, dY, gs, XA, s, g, drop, dA, dB, scl, sms, cs);
+  // 3) dA and dB "late", as in the dense backward: every operand but the keep
+  //    bits (whose readers wait for them) is complete when this launch starts,
+  //    and dX is neither read nor written by it
+  return grouped_adapter_grads(X, dY, gs, XA, s, g, drop, keep, dA, dB, scl, sms, cs);
 }

@@ -1750,7 +1750,8 @@ size_t qlora_grouped_workspace_bytes(int E, int64_t T, int64_t N, int64_t K, int
   int sms = 148;
   if (device_info(&d) == QLORA_OK) sms = d.sms;
   const GroupedPlanHost f = plan_grouped_host(s, K / 64, sms), b = plan_grouped_host(s, N / 64, sms);
-  return std::max(grouped_ws(s, f.counters, f.part, false).total, grouped_ws(s, b.counters, b.part, true).total);
+  return std::max(grouped_ws(s, f.counters, f.part, false, sms).total,
+                  grouped_ws(s, b.counters, b.part, true, sms).total);
 }
 
 qlora_status qlora_grouped_linear_fwd(const uint8_t *packed, const uint8_t *q, const float *scale2,

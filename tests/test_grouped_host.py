@@ -99,6 +99,8 @@ def test_workspace_query(lib):
     assert plain >= 2 * 1000 * 8 * 2
     # the mask is never stored and X never copied: dropout needs no scratch of its own
     assert ws(4, 1000, 1024, 2048, 8, True) == plain
+    # many rows and experts: a bit for each element, from dX to dA
+    assert ws(8, 1000, 4096, 11008, 8, True) == ws(8, 1000, 4096, 11008, 8) + 1000 * 11008 // 8
 
 
 def test_binding_refusals(lib):
