@@ -13,7 +13,8 @@
 // the expert's first row on (a row coordinate, aligned to nothing). The last
 // block may reach into the next expert's rows: warp 2 sets those rows of both
 // operands to zero in shared memory before the MMAs read them, so not even a
-// NaN there can enter. An expert without tokens gets zeros.
+// NaN there can enter. An expert without tokens has no units: its gradients
+// are set to zero by warp 3 of all CTAs.
 //
 // Dropout: dX, the launch before this one, evaluates the same mask and leaves
 // its keep bits in the workspace (T K / 8 bytes; evaluated here once more, the
@@ -22,7 +23,12 @@
 // dX and fill the SMs that its last round leaves idle; every role waits for dX
 // before its first unit of dA.
 //
-// Roles: warp 0 TMA, warp 1 TMEM + MMA, warp 2 tails, warps 4-7 readout and
+// Experts are uneven and a CTA has only a few units, so the units are handed
+// out as CTAs become free (@D@): the expert with the most tokens first, from a
+// counter in the workspace. Warp 0 takes them and passes them on through a
+// small ring. Every unit's sums are its own, so who computes it changes nothing.
+//
+// Roles: warp 0 TMA, warp 1 TMEM + MMA, warp 2 tails, warp 3 zeros, warps 4-7 readout and
 // stores, warps 8-15 (DROP) take each landed stage of X through the mask.
 #pragma once
 
@@ -39,8 +45,58 @@ struct GradientArgs {
   int K, N, r;
   int f16;
   GroupArgs groups;
-  const uint32_t *keep;  // DROP: keep bits of X, [T][K / 32], written by the kernel before this one
+  const uint32_t *keep;   // DROP: keep bits of X, [T][K / 32], written by the kernel before this one
+  unsigned int *counter;  // units taken beyond each CTA's first; zero when the launch starts
 };
+
+// The experts with tokens, by their number (to a quarter of a power of two),
+// the most first; then the others. One warp; `start`: kSizeClasses ints. Returns
+// how many have tokens. Every CTA gets the same order: within a class and a
+// step, by lane.
+constexpr int kSizeClasses = 128;
+__device__ __forceinline__ int order_by_size(const GroupTable &gt, int groups, int *start, uint16_t *order) {
+  const int lane = threadIdx.x & 31;
+  auto size_class = [&](int e) {  // 0: the most tokens, kSizeClasses - 1: none
+    if (e >= groups) return kSizeClasses;
+    const int n = gt.first[e + 1] - gt.first[e];
+    if (n == 0) return kSizeClasses - 1;
+    const int log = 31 - __clz(n), quarter = log >= 2 ? (n >> (log - 2)) & 3 : (n << (2 - log)) & 3;
+    return kSizeClasses - 2 - (4 * log + quarter);  // n < 2^31: at most 123
+  };
+  // experts of each class, then (place) where it starts
+  for (int i = lane; i < kSizeClasses; i += 32) start[i] = 0;
+  __syncwarp();
+  auto each = [&](bool place) {
+    for (int base = 0; base < groups; base += 32) {
+      const int cls = size_class(base + lane);
+      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, cls);
+      const int before = __popc(peers & ((1u << lane) - 1u));
+      const int at = cls < kSizeClasses ? start[cls] + before : 0;
+      if (place && cls < kSizeClasses) order[at] = static_cast<uint16_t>(base + lane);
+      __syncwarp();
+      if (before == 0 && cls < kSizeClasses) start[cls] += __popc(peers);
+      __syncwarp();
+    }
+  };
+  each(false);
+  int carry = 0;
+  for (int base = 0; base < kSizeClasses; base += 32) {
+    const int n = start[base + lane];
+    int sum = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    start[base + lane] = carry + sum - n;
+    carry += __shfl_sync(0xFFFFFFFFu, sum, 31);
+  }
+  __syncwarp();
+  const int some = start[kSizeClasses - 1];
+  __syncwarp();
+  each(true);
+  return some;
+}
 
 template <int BN_, int STAGES_, bool DROP_>
 struct GradientCfg {
@@ -48,11 +104,18 @@ struct GradientCfg {
   static constexpr bool DROP = DROP_;
   static constexpr int A_BYTES = 128 * 64 * 2, B_BYTES = BN_ * 64 * 2, STAGE = A_BYTES + B_BYTES;
   static constexpr int OFF_BAR = STAGES_ * STAGE;
-  // full[S] empty[S] ready[S] tmem_full[2] tmem_empty[2] landed tail drain
-  static constexpr int NBARS = 3 * STAGES_ + 7;
+  static constexpr int UNITS = 4;  // ring of the CTA's units
+  // full[S] empty[S] ready[S] tmem_full[2] tmem_empty[2] landed tail drain unit_full[U] unit_empty[U]
+  static constexpr int NBARS = 3 * STAGES_ + 7 + 2 * UNITS;
+  // misc: tmem base, abort flag, experts with tokens; the unit ring, the group
+  // table, the experts by size and the classes' starts
   static constexpr int OFF_MISC = (OFF_BAR + NBARS * 8 + 15) & ~15;
-  static constexpr int OFF_GROUPS = OFF_MISC + 16;
-  static constexpr int SMEM_BYTES = OFF_GROUPS + kGroupTableBytes;
+  static constexpr int OFF_UNITS = OFF_MISC + 16;
+  static constexpr int OFF_GROUPS = OFF_UNITS + UNITS * 4;
+  static constexpr int OFF_ORDER = OFF_GROUPS + kGroupTableBytes;
+  static constexpr int OFF_CLASSES = OFF_ORDER + kMaxGroups * 2;
+  static constexpr int SMEM_BYTES = OFF_CLASSES + kSizeClasses * 4;
+  static constexpr int UNIT_READERS = DROP_ ? 14 : 6;  // MMA, tails, readout (4), mask (8)
   static constexpr int THREADS = DROP_ ? 512 : 256;
   static constexpr uint32_t TMEM_COLS = 2 * BN_;
   static constexpr int PER_SM = SMEM_BYTES <= 113 * 1024 ? 2 : 1;
@@ -74,6 +137,10 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
   const uint32_t landed_bar = bar0 + 8u * (3 * C::STAGES + 4), tail_bar = landed_bar + 8u, drain_bar = tail_bar + 8u;
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
   volatile int *s_abort = reinterpret_cast<volatile int *>(smem + C::OFF_MISC + 4);
+  volatile int *s_unit = reinterpret_cast<volatile int *>(smem + C::OFF_UNITS);
+  uint16_t *s_order = reinterpret_cast<uint16_t *>(smem + C::OFF_ORDER);
+  auto unit_full = [&](uint32_t k) { return drain_bar + 8u + 8u * (k % C::UNITS); };
+  auto unit_empty = [&](uint32_t k) { return drain_bar + 8u + 8u * (C::UNITS + k % C::UNITS); };
   const GroupTable gt = group_table(smem + C::OFF_GROUPS);
 
   if (threadIdx.x == 0) {
@@ -89,6 +156,10 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
     mbar_init(landed_bar, 1);
     mbar_init(tail_bar, 1);
     mbar_init(drain_bar, 1);
+    for (int k = 0; k < C::UNITS; ++k) {
+      mbar_init(unit_full(k), 1);
+      mbar_init(unit_empty(k), C::UNIT_READERS);
+    }
     *s_abort = 0;
     fence_barrier_init();
   }
@@ -100,24 +171,31 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
   // when this launch starts, and nothing it writes is touched by the kernel
   // before it, for which each thread waits only before exiting.
   grid_dep_launch();
-  if (warp == 3) build_group_table(a.groups, 64, gt);
+  int *s_some = reinterpret_cast<int *>(smem + C::OFF_MISC + 8);
+  if (warp == 3) {
+    build_group_table(a.groups, 64, gt);
+    __syncwarp();
+    const int some = order_by_size(gt, a.groups.groups, reinterpret_cast<int *>(smem + C::OFF_CLASSES), s_order);
+    if (lane == 0) *s_some = some;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
 
   const int ta = (a.K + 127) / 128, tb = (a.N + 127) / 128;
-  const int nb = a.groups.groups * tb, units = nb + a.groups.groups * ta;
+  const int some = *s_some, nb = some * tb, units = nb + some * ta;
   struct Unit {
     bool second;  // dB
-    int group, row0, tok0, ntok, nk;
+    int group, row0, tok0, ntok, nk;  // nk > 0
   };
   auto unit_at = [&](int u) {
     Unit t;
     t.second = u < nb;
     const int v = t.second ? u : u - nb, per = t.second ? tb : ta;
-    t.group = v / per;
-    t.row0 = (v - t.group * per) * 128;
+    const int at = v / per;
+    t.group = s_order[at];
+    t.row0 = (v - at * per) * 128;
     t.tok0 = gt.first[t.group];
     t.ntok = gt.first[t.group + 1] - t.tok0;
     t.nk = (t.ntok + 63) / 64;
@@ -133,12 +211,35 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
     }
   };
 
+  // the CTA's k-th unit (a warp, or the one thread of a role); false: there are no more
+  auto take_warp = [&](uint32_t k, Unit &t) -> bool {
+    if (!warp_wait_all(unit_full(k), (k / C::UNITS) & 1u, s_abort)) return false;
+    const int u = s_unit[k % C::UNITS];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(unit_empty(k));
+    if (u < units) t = unit_at(u);
+    return u < units;
+  };
+  auto take_thread = [&](uint32_t k, Unit &t) -> bool {
+    if (!mbar_wait(unit_full(k), (k / C::UNITS) & 1u, s_abort)) return false;
+    const int u = s_unit[k % C::UNITS];
+    mbar_arrive(unit_empty(k));
+    if (u < units) t = unit_at(u);
+    return u < units;
+  };
+
+  Unit t;
   if (warp == 0) {
     if (elect_one()) {
       uint32_t it = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-        const Unit t = unit_at(u);
+      int u = blockIdx.x;
+      for (uint32_t k = 0; ok; ++k) {
+        if (!mbar_wait(unit_empty(k), ((k / C::UNITS) & 1u) ^ 1u, s_abort)) break;
+        s_unit[k % C::UNITS] = u;
+        mbar_arrive(unit_full(k));
+        if (u >= units) break;
+        t = unit_at(u);
         wait_dx(t);
         const CUtensorMap *ma = t.second ? &a.tm_dy : &a.tm_x, *mb = t.second ? &a.tm_xa : &a.tm_gs;
         for (int j = 0; j < t.nk; ++j, ++it) {
@@ -151,6 +252,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
 #pragma unroll
           for (int c = 0; c < C::BN / 64; ++c) tma_load_2d(dst + C::A_BYTES + c * 8192, mb, full_bar(s), c * 64, tok);
         }
+        u = static_cast<int>(gridDim.x + atomicAdd(a.counter, 1u));
       }
       // wait (bounded) for the copies still in flight
       const uint32_t inflight = it < static_cast<uint32_t>(C::STAGES) ? it : C::STAGES;
@@ -166,14 +268,12 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
   } else if (warp == 1) {
     if (elect_one()) {
       const uint32_t idesc = idesc_dtype(make_idesc_bf16(128, C::BN, 1, 1), a.f16);
-      uint32_t it = 0, use = 0, tails = 0;
+      uint32_t it = 0, tails = 0;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-        const Unit t = unit_at(u);
+      for (uint32_t k = 0; ok && take_thread(k, t); ++k) {
         wait_dx(t);
-        if (t.nk == 0) continue;
-        const int b = use & 1u;
-        if (!mbar_wait(tmem_empty(b), ((use >> 1) & 1u) ^ 1u, s_abort)) { ok = false; break; }
+        const int b = k & 1u;
+        if (!mbar_wait(tmem_empty(b), ((k >> 1) & 1u) ^ 1u, s_abort)) { ok = false; break; }
         tc_fence_after();
         for (int j = 0; j < t.nk; ++j, ++it) {
           const int s = it % C::STAGES;
@@ -193,7 +293,6 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
         }
         if (!ok) break;
         tc_commit(tmem_full(b));
-        ++use;
       }
       if (it > 0) {
         tc_commit(drain_bar);
@@ -206,8 +305,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
     __syncwarp();
   } else if (warp == 2) {
     uint32_t it = 0, tails = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-      const Unit t = unit_at(u);
+    for (uint32_t k = 0; take_warp(k, t); ++k) {
       wait_dx(t);
       it += t.nk;
       const int rows = t.ntok & 63;
@@ -230,28 +328,19 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
   } else if (warp >= 4 && warp < 8) {
     const int q = warp - 4;
     const bool f16 = a.f16 != 0;
-    uint32_t use = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
-      const Unit t = unit_at(u);
-      const int b = use & 1u;
+    for (uint32_t k = 0; take_warp(k, t); ++k) {
+      const int b = k & 1u;
       wait_dx(t);
-      if (t.nk > 0) {
-        if (!warp_wait_all(tmem_full(b), (use >> 1) & 1u, s_abort)) break;
-        tc_fence_after();
-      }
+      if (!warp_wait_all(tmem_full(b), (k >> 1) & 1u, s_abort)) break;
+      tc_fence_after();
       const int base = t.row0 + q * 32;  // K and N are multiples of 64: 32 rows or none
 #pragma unroll 1
       for (int c0 = 0; c0 < a.r && base < (t.second ? a.N : a.K); c0 += 32) {
+        uint32_t w[32];
+        tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * C::BN + c0, w);
         float v[32];
-        if (t.nk > 0) {
-          uint32_t w[32];
-          tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * C::BN + c0, w);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]) * (t.second ? a.b_scale : 1.0f);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-        }
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]) * (t.second ? a.b_scale : 1.0f);
         if (!t.second) {  // a row of dA per lane
           uint16_t *dst = reinterpret_cast<uint16_t *>(a.dA) +
                           (static_cast<int64_t>(t.group) * a.K + base + lane) * a.r + c0;
@@ -274,12 +363,20 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
           }
         }
       }
-      if (t.nk > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(tmem_empty(b));
-        ++use;
-      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tmem_empty(b));
+    }
+  } else if (warp == 3) {
+    // the gradients of the experts without tokens, consecutive bytes each
+    auto zero = [&](void *grad, int e, int64_t elements) {
+      uint8_t *dst = static_cast<uint8_t *>(grad) + e * elements * 2;
+      for (int64_t i = (blockIdx.x * 32 + lane) * 16; i < elements * 2; i += gridDim.x * 512)
+        *reinterpret_cast<uint4 *>(dst + i) = make_uint4(0u, 0u, 0u, 0u);
+    };
+    for (int at = some; at < a.groups.groups; ++at) {
+      zero(a.dA, s_order[at], static_cast<int64_t>(a.K) * a.r);
+      zero(a.dB, s_order[at], static_cast<int64_t>(a.N) * a.r);
     }
   } else if (C::DROP && warp >= 8) {
     // M o X. 16-byte piece c of row r of a 64-wide chunk lies at c ^ (r & 7)
@@ -293,8 +390,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
     const int64_t ld = a.K / 32;
     uint32_t it = 0;
     bool ok = true;
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-      const Unit t = unit_at(u);
+    for (uint32_t k = 0; ok && take_warp(k, t); ++k) {
       wait_dx(t);
       const uint32_t *bits = a.keep + static_cast<int64_t>(t.tok0 + r) * ld + t.row0 / 32 + word;
       const bool in_row = t.row0 / 32 + word < ld;

@@ -69,7 +69,7 @@ GroupedPlanHost plan_grouped_host(const GroupedShape &s, int64_t kblocks, int sm
   GroupedPlanHost p{};
   p.ntt = s.T / s.E >= kGroupedTwoSubtile ? 2 : 1;
   p.slots = grouped_pair_slots(sms);
-  p.counters = 2 * p.slots;
+  p.counters = 2 * p.slots + 1;  // of split tiles, and of gradient_kernel's units
   p.part = grouped_part_bytes(p.slots, p.ntt, kblocks);
   return p;
 }
@@ -221,8 +221,9 @@ qlora_status run_gradients(const GradientArgs &a, int64_t units, int sms, cudaSt
 // launch: over persistent CTAs (`keep`: the mask's bits, which dX left), else
 // with each tile's tokens split over a cluster.
 qlora_status grouped_adapter_grads(const void *X, const void *dY, const void *gs, const void *xa, const GroupedShape &s,
-                                   const GroupArgs &g, const DropoutArgs &drop, const uint32_t *keep, void *dA,
-                                   void *dB, float b_scale, int sms, cudaStream_t st) {
+                                   const GroupArgs &g, const DropoutArgs &drop, const uint32_t *keep,
+                                   unsigned int *unit_counter, void *dA, void *dB, float b_scale, int sms,
+                                   cudaStream_t st) {
   const int64_t ta = s.E * cdiv(s.K, 128), tb = s.E * cdiv(s.N, 128);
   if (persistent_gradients(s, sms)) {
     GradientArgs a;
@@ -239,6 +240,7 @@ qlora_status grouped_adapter_grads(const void *X, const void *dY, const void *gs
     a.f16 = t_f16 ? 1 : 0;
     a.groups = g;
     a.keep = keep;
+    a.counter = unit_counter;
     return s.drop ? run_gradients<true>(a, ta + tb, sms, st) : run_gradients<false>(a, ta + tb, sms, st);
   }
   SkinnyPlan p;
@@ -406,5 +408,5 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
   // 3) dA and dB "late", as in the dense backward: every operand but the keep
   //    bits (whose readers wait for them) is complete when this launch starts,
   //    and dX is neither read nor written by it
-  return grouped_adapter_grads(X, dY, gs, XA, s, g, drop, keep, dA, dB, scl, sms, cs);
+  return grouped_adapter_grads(X, dY, gs, XA, s, g, drop, keep, counters + 2 * p.slots, dA, dB, scl, sms, cs);
 }

@@ -136,6 +136,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
   if constexpr (C::GROUPED) {
     // late launches run on inputs that are complete when they start
     if (!args.late) grid_dep_wait();
+    if (blockIdx.x == 0)  // (before a launch without tokens leaves)
+      for (int i = threadIdx.x; i < args.nzero; i += blockDim.x) args.zero_words[i] = 0u;
     const GroupTable gt = group_table(smem + C::OFF_GROUPS);
     if (warp == 0) build_group_table(args.groups, 128, gt);
     __syncthreads();
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
     for (; issued < nk && issued < C::STAGES; ++issued) issue(issued);
   if (!C::GROUPED && !args.late) grid_dep_wait();
   grid_dep_launch();
-  if (blockIdx.x == 0)
+  if (!C::GROUPED && blockIdx.x == 0)
     for (int i = threadIdx.x; i < args.nzero; i += blockDim.x) args.zero_words[i] = 0u;
 
   if (warp == 0) {
