@@ -133,36 +133,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
   int kblocks = P.kblocks;
   int group = 0;           // expert
   int tok0 = 0, ntok = 0;  // products over the tokens: the expert's first token and count
+  const GroupTable gt = group_table(smem + C::OFF_GROUPS);
+  if (warp == 3 && lane == 0) {
+    tma_prefetch_desc(&P.tm_a);
+    tma_prefetch_desc(&P.tm_b);
+  }
   if constexpr (C::GROUPED) {
     // late launches run on inputs that are complete when they start
     if (!args.late) grid_dep_wait();
     if (blockIdx.x == 0)  // (before a launch without tokens leaves)
       for (int i = threadIdx.x; i < args.nzero; i += blockDim.x) args.zero_words[i] = 0u;
-    const GroupTable gt = group_table(smem + C::OFF_GROUPS);
-    if (warp == 0) build_group_table(args.groups, 128, gt);
-    __syncthreads();
-    if constexpr (C::A_MN) {
-      const int row_tiles = (P.rows + 127) / 128;
-      group = tile / row_tiles;
-      row0 = (tile - group * row_tiles) * 128;
-      tok0 = gt.first[group];
-      ntok = gt.first[group + 1] - tok0;
-      kblocks = (ntok + 63) / 64;
-    } else {
-      if (tile >= gt.cum[args.groups.groups]) {  // the whole cluster leaves
-        grid_dep_launch();
-        return;
-      }
-      group = group_of_tile(gt, args.groups.groups, tile);
-      row0 = gt.first[group] + (tile - gt.cum[group]) * 128;
-      row_end = gt.first[group + 1];
-    }
+    if (warp == 2) build_group_table(args.groups, 128, gt);  // beside the barriers and TMEM below
   }
-  const int kb_begin = static_cast<int>((static_cast<int64_t>(rank) * kblocks) / splits);
-  const int kb_end = static_cast<int>((static_cast<int64_t>(rank + 1) * kblocks) / splits);
-  const int nk = kb_end - kb_begin;
-  // this CTA's last block ends inside: its rows past the expert's last token are zeroed
-  const int tail_rows = C::GROUPED && C::A_MN && nk > 0 && kb_end == kblocks ? ntok & 63 : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -179,10 +161,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
     *s_abort = 0;
     fence_barrier_init();
   }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&P.tm_a);
-    tma_prefetch_desc(&P.tm_b);
-  }
   if (warp == 1) {
     tmem_alloc(smem_u32(s_tmem), C::TMEM_COLS);
     tmem_relinquish();
@@ -191,6 +169,31 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
+  if constexpr (C::GROUPED) {
+    if constexpr (C::A_MN) {
+      const int row_tiles = (P.rows + 127) / 128;
+      group = tile / row_tiles;
+      row0 = (tile - group * row_tiles) * 128;
+      tok0 = gt.first[group];
+      ntok = gt.first[group + 1] - tok0;
+      kblocks = (ntok + 63) / 64;
+    } else {
+      if (tile >= gt.cum[args.groups.groups]) {  // the whole cluster leaves
+        if (warp == 1) tmem_dealloc(tmem_base, C::TMEM_COLS);
+        grid_dep_launch();
+        return;
+      }
+      group = group_of_tile(gt, args.groups.groups, tile);
+      row0 = gt.first[group] + (tile - gt.cum[group]) * 128;
+      row_end = gt.first[group + 1];
+    }
+  }
+  const int kb_begin = static_cast<int>((static_cast<int64_t>(rank) * kblocks) / splits);
+  const int kb_end = static_cast<int>((static_cast<int64_t>(rank + 1) * kblocks) / splits);
+  const int nk = kb_end - kb_begin;
+  // this CTA's last block ends inside: its rows past the expert's last token are zeroed
+  const int tail_rows = C::GROUPED && C::A_MN && nk > 0 && kb_end == kblocks ? ntok & 63 : 0;
+
   // producer state: stages issued so far (the first ring's worth may go out
   // ahead of the wait for the previous kernel, see SkinnyArgs::early)
   int issued = 0;
