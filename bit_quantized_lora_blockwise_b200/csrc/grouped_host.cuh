@@ -7,10 +7,11 @@
 // the tile from the average tokens per expert; either is right for every
 // split.
 
-// An expert of c tokens has ceil(c / tile) token tiles: at most T / tile full
-// ones in all and one partial one per expert with tokens.
+// An expert of c tokens has ceil(c / tile) token tiles: the most there can be
+// is when each of the experts has one token and the rest fills whole tiles.
 inline int64_t token_tiles_bound(int64_t T, int64_t E, int64_t tile) {
-  return std::min(T, T / tile + std::min(E, T));
+  const int64_t experts = std::min(E, T);
+  return experts + (T - experts) / tile;
 }
 
 struct GroupedShape {

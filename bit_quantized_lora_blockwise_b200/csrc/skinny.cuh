@@ -318,28 +318,46 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
     if constexpr (C::DROP) {
       // M o X, stage by stage. 16-byte piece c of row r of a 64-wide K-major
       // (or MN-major) chunk lies at c ^ (r & 7) in the row's 128 bytes. A
-      // thread's four pieces are 32 rows apart; their masks are formed side
-      // by side before the stage is waited for. Rows of no token of this
-      // expert are masked too: never stored (K-major) or zeroed by warp 2.
+      // thread's four pieces are 32 rows apart; their masks are formed side by
+      // side, two before and two after the stage before theirs is masked, so
+      // that the shared-memory accesses (256 clocks a stage, beside some 1000
+      // for the generator's wide products) and the fence pass meanwhile. Rows
+      // of no token of this expert are masked too: never stored (K-major) or
+      // zeroed by warp 2.
       const int tid = q * 32 + lane, c = tid & 7, r0 = tid >> 3;
       const uint32_t swz = static_cast<uint32_t>(c ^ (r0 & 7)) << 4;  // (the same for rows 32 apart)
       const uint64_t ld8 = static_cast<uint64_t>(args.drop_ld) / 8;
-      for (int j = 0; P.masked && j < nk; ++j) {
-        const int s = j % C::STAGES, kb = kb_begin + j;
-        // counter of the piece in row r0: K-major 128 token rows of one chunk, MN-major 64 token rows of two
+      uint4 mask[4];  // of the stage at hand
+      // masks i0 and i0 + 1 of stage j. Counter of the piece in row r0:
+      // K-major 128 token rows of one chunk, MN-major 64 token rows of two
+      auto masks = [&](int j, int i0, uint4 (&m)[4]) {
+        const int kb = kb_begin + j;
         const uint64_t first = C::A_MN ? static_cast<uint64_t>(tok0 + kb * 64 + r0) * ld8 + (row0 / 8 + c)
                                        : static_cast<uint64_t>(row0 + r0) * ld8 + (kb * 8 + c);
-        uint4 mask[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          mask[i] = dropout_mask8(args.drop, first + (C::A_MN ? (i & 1) * 32 * ld8 + (i >> 1) * 8 : i * 32 * ld8));
+        for (int i = i0; i < i0 + 2; ++i)
+          m[i] = dropout_mask8(args.drop, first + (C::A_MN ? (i & 1) * 32 * ld8 + (i >> 1) * 8 : i * 32 * ld8));
+      };
+      if (P.masked && nk > 0) {
+        masks(0, 0, mask);
+        masks(0, 2, mask);
+      }
+      for (int j = 0; P.masked && j < nk; ++j) {
+        const int s = j % C::STAGES;
         if (!warp_wait_all(full_bar(s), (j / C::STAGES) & 1u, s_abort)) break;
         uint8_t *piece = smem + C::OFF_A + s * C::A_BYTES + r0 * 128 + swz;
+        uint4 v[4], next[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4 *at = reinterpret_cast<uint4 *>(piece + i * 4096);
-          const uint4 v = *at;
-          *at = make_uint4(v.x & mask[i].x, v.y & mask[i].y, v.z & mask[i].z, v.w & mask[i].w);
+        for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4 *>(piece + i * 4096);
+        if (j + 1 < nk) masks(j + 1, 0, next);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4 *>(piece + i * 4096) =
+              make_uint4(v[i].x & mask[i].x, v[i].y & mask[i].y, v[i].z & mask[i].z, v[i].w & mask[i].w);
+        if (j + 1 < nk) {
+          masks(j + 1, 2, next);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mask[i] = next[i];
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -387,6 +405,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
         lr = u / c4n;
         c4 = u - lr * c4n;
       }
+      if (c4 * 4 >= P.cols) continue;  // (a multiple of 8: four columns or none)
       const int lrow = static_cast<int>(rank) * R + lr;
       const uint32_t off = static_cast<uint32_t>((lrow * C::PART_LD + c4 * 4) * 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -416,13 +435,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
         if constexpr (C::GROUPED && C::A_MN) dst += static_cast<int64_t>(group) * P.rows * P.cols;  // this expert's
         const float sc = o ? P.out2_scale : P.out_scale;
         const int64_t ld = o ? P.out2_ld : P.out_ld;
+        const bool f16 = args.f16 != 0;
+        if (P.transpose) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int col = c4 * 4 + e;
-          if (col >= P.cols) continue;
-          const int64_t idx = P.transpose ? static_cast<int64_t>(col) * ld + row
-                                             : static_cast<int64_t>(row) * ld + col;
-          dst[idx] = to_16(vv[e] * sc, args.f16 != 0);
+          for (int e = 0; e < 4; ++e) dst[static_cast<int64_t>(c4 * 4 + e) * ld + row] = to_16(vv[e] * sc, f16);
+        } else {
+          *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(row) * ld + c4 * 4) =
+              make_uint2(pack_16x2(vv[0] * sc, vv[1] * sc, f16), pack_16x2(vv[2] * sc, vv[3] * sc, f16));
         }
       }
     }
