@@ -20,6 +20,8 @@ struct DropoutArgs {
   uint32_t key[10][2];  // the rounds' keys, formed once on the host: constant operands of the rounds' xors
   uint64_t offset;
   uint32_t threshold;  // 0: nothing is dropped
+  uint32_t both;       // the threshold in both halves
+  uint32_t low15;      // and its lower 15 bits
   float factor;        // 2^16 / (2^16 - threshold)
 };
 
@@ -32,6 +34,8 @@ inline DropoutArgs dropout_args(uint64_t seed, uint64_t offset, uint32_t thresho
   }
   d.offset = offset;
   d.threshold = threshold;
+  d.both = threshold << 16 | threshold;
+  d.low15 = d.both & 0x7FFF7FFFu;
   d.factor = static_cast<float>(65536.0 / (65536.0 - threshold));
   return d;
 }
@@ -53,49 +57,44 @@ __device__ __forceinline__ uint4 philox4x32_10(const DropoutArgs &d, uint64_t co
   return make_uint4(c0, c1, c2, c3);
 }
 
-// Whether the elements of a word's low and high half are kept.
-__device__ __forceinline__ void keep_pair(uint32_t word, uint32_t threshold, bool &lo, bool &hi) {
-  hi = word >= threshold << 16;
-  lo = word << 16 >= threshold << 16;
+// Both halves of a word against the threshold at once: bit 15 and bit 31 tell
+// whether the low and the high half are kept (the other bits are of no use).
+// With the top bit forced, a subtraction compares the 15 bits below it without
+// a borrow between the halves; the top bits themselves decide where they
+// differ. Three integer operations where two compares of shifted halves, with
+// their selects, take six.
+__device__ __forceinline__ uint32_t keep_signs(const DropoutArgs &d, uint32_t word) {
+  const uint32_t z = (word | 0x80008000u) - d.low15;
+  return (word & ~d.both) | (~(word ^ d.both) & z);
 }
 
 // Keep bits of the eight elements of one counter (bit j: element j).
 __device__ __forceinline__ uint32_t dropout_keep8(const DropoutArgs &d, uint64_t group) {
   const uint4 w = philox4x32_10(d, d.offset + group);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-  uint32_t keep = 0u;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    bool lo, hi;
-    keep_pair(u[j], d.threshold, lo, hi);
-    keep |= (lo ? 1u << (2 * j) : 0u) | (hi ? 2u << (2 * j) : 0u);
-  }
-  return keep;
+  // four elements a word, a byte of ones or zeros each (the signs of bytes 1
+  // and 3), a bit of each byte kept, the four bytes added up
+  const uint32_t lo = prmt(keep_signs(d, w.x), keep_signs(d, w.y), 0xFDB9u);
+  const uint32_t hi = prmt(keep_signs(d, w.z), keep_signs(d, w.w), 0xFDB9u);
+  return (((lo & 0x08040201u) | (hi & 0x80402010u)) * 0x01010101u) >> 24;
 }
 
 // The same as masks of the four words of eight 16-bit elements.
 __device__ __forceinline__ uint4 dropout_mask8(const DropoutArgs &d, uint64_t group) {
   const uint4 w = philox4x32_10(d, d.offset + group);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-  uint32_t m[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    bool lo, hi;
-    keep_pair(u[j], d.threshold, lo, hi);
-    m[j] = (lo ? 0x0000FFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
-  }
-  return make_uint4(m[0], m[1], m[2], m[3]);
+  auto mask = [&](uint32_t word) {
+    const uint32_t s = keep_signs(d, word);
+    return prmt(s, s, 0xBB99u);
+  };
+  return make_uint4(mask(w.x), mask(w.y), mask(w.z), mask(w.w));
 }
 
 enum DropoutType : int { DROP_BF16 = 0, DROP_F16 = 1, DROP_F32 = 2 };
 
-// Two elements of a word's halves: kept ones times the factor (fp32 product,
-// one rounding), the others +0, whatever they held (a dropped NaN or infinity
-// is 0).
+// Two elements of a word's halves, masked: times the factor (fp32 product, one
+// rounding). A dropped element is +0, whatever it held (NaN and infinity too).
 template <int TYPE>
-__device__ __forceinline__ uint32_t dropout_pair(uint32_t v, bool klo, bool khi, float factor) {
-  v = klo ? v : v & 0xFFFF0000u;
-  v = khi ? v : v & 0x0000FFFFu;
+__device__ __forceinline__ uint32_t dropout_pair(uint32_t v, uint32_t mask, float factor) {
+  v &= mask;
   float lo, hi;
   if constexpr (TYPE == DROP_F16) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v));
@@ -106,21 +105,6 @@ __device__ __forceinline__ uint32_t dropout_pair(uint32_t v, bool klo, bool khi,
     hi = __uint_as_float(v & 0xFFFF0000u);
   }
   return pack_16x2(lo * factor, hi * factor, TYPE == DROP_F16);
-}
-
-// The same for the eight elements of one counter.
-template <int TYPE>
-__device__ __forceinline__ uint4 dropout_eight(const uint4 &v, const DropoutArgs &d, uint64_t group, float factor) {
-  const uint4 w = philox4x32_10(d, d.offset + group);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w}, x[4] = {v.x, v.y, v.z, v.w};
-  uint32_t y[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    bool lo, hi;
-    keep_pair(u[j], d.threshold, lo, hi);
-    y[j] = dropout_pair<TYPE>(x[j], lo, hi, factor);
-  }
-  return make_uint4(y[0], y[1], y[2], y[3]);
 }
 
 // y[i] = keep(i) ? x[i] * factor : 0 over n elements; x and y 16-byte
@@ -147,7 +131,10 @@ __global__ void __launch_bounds__(256) dropout_kernel(const void *x, void *y, in
                       k & 128u ? b.w * factor : 0.0f);
     } else {
       const uint4 v = reinterpret_cast<const uint4 *>(x)[g];
-      reinterpret_cast<uint4 *>(y)[g] = dropout_eight<TYPE>(v, d, static_cast<uint64_t>(g), factor);
+      const uint4 m = dropout_mask8(d, static_cast<uint64_t>(g));
+      reinterpret_cast<uint4 *>(y)[g] =
+          make_uint4(dropout_pair<TYPE>(v.x, m.x, factor), dropout_pair<TYPE>(v.y, m.y, factor),
+                     dropout_pair<TYPE>(v.z, m.z, factor), dropout_pair<TYPE>(v.w, m.w, factor));
     }
   }
   // the last, partial counter: one thread, element by element
@@ -161,7 +148,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const void *x, void *y, in
         reinterpret_cast<float *>(y)[i] = (k >> j) & 1u ? v * factor : 0.0f;
       } else {
         const uint32_t v = reinterpret_cast<const uint16_t *>(x)[i];
-        reinterpret_cast<uint16_t *>(y)[i] = static_cast<uint16_t>(dropout_pair<TYPE>(v, (k >> j) & 1u, true, factor));
+        reinterpret_cast<uint16_t *>(y)[i] = static_cast<uint16_t>(dropout_pair<TYPE>(v, (k >> j) & 1u ? 0xFFFFu : 0u, factor));
       }
     }
   }
