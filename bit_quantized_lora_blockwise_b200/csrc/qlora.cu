@@ -530,9 +530,17 @@ qlora_status plan_skinny_v(int64_t rows, int64_t kdim, int r, SkinnyPlan *p) {
                           : p->bn == 128 ? SkinnyVariant<128, AMN, BMN, GROUPED, DROP>::prepare(maxc, &p->per_sm)
                                          : SkinnyVariant<256, AMN, BMN, GROUPED, DROP>::prepare(maxc, &p->per_sm);
   const int row_tiles = static_cast<int>(cdiv(rows, 128));
+  // The occupancy queries count one CTA per SM for a kernel that allocates TMEM,
+  // though two share one where their shared memory allows it (BN up to 128):
+  // the masked X A, which the generator's arithmetic binds, counts both (2048 rows
+  // of 4096 as 128 CTAs, not 64: 19.8 us, not 22.8). The others are better off
+  // leaving SMs to the GEMM that starts beside them (backward of 2048 rows of
+  // 11008 x 4096: dY B^T on 128 CTAs 189 us, on 64 186; dA and dB split
+  // further end 10 us later).
+  const int per_sm = DROP && !AMN && p->bn <= 128 ? 2 : 1;
   p->splits = 1;
   for (int l = 3; l >= 1; --l)
-    if ((1 << l) <= p->kblocks && row_tiles <= maxc[l]) {
+    if ((1 << l) <= p->kblocks && row_tiles <= per_sm * maxc[l]) {
       p->splits = 1 << l;
       break;
     }

@@ -101,7 +101,7 @@ struct SkinnyCfg {
   static constexpr uint32_t TMEM_COLS = BN_ <= 64 ? 64 : (BN_ <= 128 ? 128 : 256);
   static constexpr int PART_LD = BN_ + 4;  // fp32 per partial row (16-byte pad against bank conflicts)
   static_assert(128 * PART_LD * 4 <= OFF_BAR, "the partial reuses the ring");
-  static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
+  static_assert(SMEM_BYTES <= (BN_ <= 128 ? 113 * 1024 : 232448), "shared memory per CTA: two on an SM up to rank 128");
   static constexpr uint32_t TX = A_BYTES + B_BYTES;
 };
 
