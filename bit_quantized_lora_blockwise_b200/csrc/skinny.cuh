@@ -321,7 +321,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
       // thread's four pieces are 32 rows apart; their masks are formed side by
       // side, two before and two after the stage before theirs is masked, so
       // that the shared-memory accesses (256 clocks a stage, beside some 1000
-      // for the generator's wide products) and the fence pass meanwhile. Rows
+      // for the generator, whose instructions fill the issue slots) and the
+      // fence pass meanwhile. Rows
       // of no token of this expert are masked too: never stored (K-major) or
       // zeroed by warp 2.
       const int tid = q * 32 + lane, c = tid & 7, r0 = tid >> 3;

@@ -497,8 +497,9 @@ QLORA_API qlora_status qlora_dropout(const void *x, void *y, int64_t n, qlora_el
  *   XA_out may be NULL (not saved); XA may be NULL (recomputed from X).
  *   workspace: at least qlora_grouped_workspace_bytes(E, T, N, K, r, dropout)
  *     bytes (enough for either direction; dropout: nonzero when `drop` will
- *     be given, though it needs no scratch of its own at present). Calls that
- *     may overlap on the device need a workspace each.
+ *     be given: with many experts and rows a backward leaves the mask's bits
+ *     there between its launches). Calls that may overlap on the device need
+ *     a workspace each.
  * Accumulation is fp32; s X A and G are rounded to 16 bits before their
  * rank-r products, everything else once. Experts are isolated: a NaN or an
  * infinity in one expert's rows or adapters reaches that expert's outputs

@@ -329,6 +329,44 @@ def test_graph_replay_with_other_offsets(counts):
     assert binding.device_error() == 0
 
 
+@pytest.mark.parametrize("drop", [None, binding.Dropout(0.3, 11)])
+def test_graph_replay_with_many_tiles(drop):
+    """The same with more adapter-gradient tiles than resident CTAs: uneven, one expert, none, and the first ones again."""
+    E, T = 36, 700
+    L = Layer([T // E] * E, 704, 576, 8, seed=12, trail=T - T // E * E, std=0.02)
+    dX = torch.zeros(T, L.K, dtype=BF, device="cuda")
+    dA, dB = torch.empty_like(L.A), torch.empty_like(L.B)
+    ws = torch.empty(binding.grouped_workspace_bytes(E, T, L.N, L.K, L.r, drop is not None), dtype=torch.uint8,
+                     device="cuda")
+
+    def step():
+        binding.grouped_linear_bwd(*L.weight, L.X, L.dY, L.offsets, L.A, L.B, L.alpha, L.N, L.K, XA=None, dX=dX, dA=dA,
+                                   dB=dB, workspace=ws, dropout=drop)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    rng = np.random.default_rng(3)
+    uneven = [0, *sorted(rng.integers(0, T + 1, E - 1).tolist()), T]
+    for off in (uneven, [0] * 20 + [T] * (E - 19), [5] * (E + 1), L.off, uneven):
+        L.offsets.copy_(torch.tensor(off, dtype=torch.int32))
+        L.off = off
+        dX.fill_(7)
+        dA.fill_(7)
+        dB.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (dX, dA, dB)]
+        for e in range(E):
+            if off[e] == off[e + 1]:
+                assert not got[1][e].any() and not got[2][e].any()
+        assert all(torch.equal(a, b) for a, b in zip(got, L.bwd(None, drop)))
+        check(L, drop, save_xa=False)
+    assert binding.device_error() == 0
+
+
 def test_two_streams_at_once():
     """Two calls in flight, a workspace each, on side streams."""
     Ls = [Layer(c, 448, 512, 16, seed=i) for i, c in enumerate(([300, 410, 77], [6, 8, 2]))]
