@@ -97,7 +97,7 @@ def test_workspace_query(lib):
     assert ws(4, 0, 128, 128, 8) > 0
     plain = ws(4, 1000, 1024, 2048, 8)
     assert plain >= 2 * 1000 * 8 * 2
-    # the mask is never stored and X never copied: dropout needs no scratch of its own
+    # no call keeps the mask and X is never copied: with few tiles dropout needs no scratch of its own
     assert ws(4, 1000, 1024, 2048, 8, True) == plain
     # many rows and experts: a bit for each element, from dX to dA
     assert ws(8, 1000, 4096, 11008, 8, True) == ws(8, 1000, 4096, 11008, 8) + 1000 * 11008 // 8
