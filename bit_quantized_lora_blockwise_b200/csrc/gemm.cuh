@@ -364,7 +364,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
   // accumulator half it has read) is ready; only its own SM's tensor core
   // touches that memory next, so the arrival carries the default CTA-scope
   // release. (A cluster-scope release here cost a third of the kernel's
-  // throughput on B200.)
+  // throughput on B200.) The one arrival after which the leader's MMAs read
+  // what warps of the peer wrote to TMEM, once a tile, is masked(): it releases
+  // at cluster scope.
   auto arrive_leader = [&](uint32_t bar) {
     if constexpr (C::PAIR) mbar_arrive_remote(map_cluster(bar, 0u));
     else mbar_arrive(bar);
@@ -687,7 +689,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
           for (int st = 0; st < C::NTT; ++st) {  // the low-rank sums have been masked
             const uint32_t acc = (u0 + st) & 1u;
             if (!active[st]) continue;
-            ok = ok && wait_full(masked(acc), (mph >> acc) & 1u);
+            ok = ok && mbar_wait_cluster(masked(acc), (mph >> acc) & 1u, s_abort);
             mph ^= 1u << acc;
           }
           if (!ok) break;
@@ -790,7 +792,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_leader(masked(acc));
+          // what the peer's warps wrote to its TMEM is read by MMAs that the
+          // leader issues: cluster scope, on both sides
+          if (lane == 0) mbar_arrive_cluster(map_cluster(masked(acc), 0u));
         }
         if (!ok) continue;
         keep_words(tile + tile_step);  // of the next tile, while this one runs
