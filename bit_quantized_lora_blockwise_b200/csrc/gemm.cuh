@@ -72,9 +72,10 @@
 // Adapter dropout in dX (DROP = true): dX = dY W' + D'(G A^T), the mask acting
 // on the low-rank sum alone. That sum is therefore formed first: the
 // low-rank K blocks run before the main ones, the epilogue warps take the
-// accumulator out of TMEM, zero what is dropped and put it back, and the main
-// K blocks accumulate on top. No second accumulator, no pass over dX, no
-// rounding of the term. A warp's 32 rows are four Philox counters of 8
+// accumulator out of TMEM, zero what is dropped, multiply the rest by the
+// factor (in fp32: factor G need not fit the 16-bit type) and put it back, and
+// the main K blocks accumulate on top. No second accumulator, no pass over dX,
+// no rounding of the term. A warp's 32 rows are four Philox counters of 8
 // consecutive k, so lane j evaluates the four counters of token j (32 keep
 // bits, one per row), and a bit transpose gives each row its word. The words
 // of a tile are evaluated while the tile before it runs.
@@ -125,7 +126,7 @@ struct GemmArgs {
   // expert-grouped calls only
   GroupArgs groups;
   int expert_rows;    // N: weight rows of one expert
-  DropoutArgs drop;   // DROP: the adapter dropout of dX, over [tokens, rows] (its factor is in B2)
+  DropoutArgs drop;   // DROP: the adapter dropout of dX, over [tokens, rows]
   uint32_t *keep_bits;  // DROP, optional: the keep bits it evaluates, [tokens][rows / 32], for dA
 };
 
@@ -787,7 +788,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) qgemm_kernel(const __grid_const
             tmem_ld_32x32b_x32(tcol + ch * 32, w);
             const uint32_t word = keep[st * C::NCHUNK + ch];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) w[j] = (word >> j) & 1u ? w[j] : 0u;
+            for (int j = 0; j < 32; ++j)
+              w[j] = (word >> j) & 1u ? __float_as_uint(__uint_as_float(w[j]) * args.drop.factor) : 0u;
             tmem_st_32x32b_x32(tcol + ch * 32, w);
           }
           tc_fence_before();

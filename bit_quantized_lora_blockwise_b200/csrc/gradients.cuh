@@ -1,6 +1,6 @@
 // Adapter gradients of many experts in one persistent launch:
-//   dA_e = (M o X_e)^T Gs_e   [K, r],      dB_e = s (XA_e^T dY_e)   [r, N]
-// (M: the dropout mask, 1 without dropout), each the product over the
+//   dA_e = f (M o X_e)^T Gs_e   [K, r],    dB_e = s (XA_e^T dY_e)   [r, N]
+// (M, f: the dropout mask and factor, 1 without dropout), each the product over the
 // expert's tokens alone. skinny_kernel computes the same sums with one
 // cluster per tile, split over the tokens; with more tiles than resident CTAs
 // its cost is the CTA itself (tables, TMEM, first copies, shared-memory
@@ -42,7 +42,7 @@ struct GradientArgs {
   CUtensorMap tm_x, tm_gs;   // X [T, K], Gs [T, r]: 64 x 64 boxes
   CUtensorMap tm_dy, tm_xa;  // dY [T, N], XA [T, r]
   void *dA, *dB;             // [E, K, r], [E, r, N], 16-bit
-  float b_scale;             // s
+  float a_scale, b_scale;    // f, s
   int K, N, r;
   int f16;
   GroupArgs groups;
@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
     const bool f16 = a.f16 != 0;
     for (uint32_t k = 0; take_warp(k, t); ++k) {
       const int b = k & 1u;
+      const float scale = t.second ? a.b_scale : a.a_scale;
       wait_dx(t);
       if (!warp_wait_all(tmem_full(b), (k >> 1) & 1u, s_abort)) break;
       tc_fence_after();
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
         tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * C::BN + c0, w);
         float v[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]) * (t.second ? a.b_scale : 1.0f);
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]) * scale;
         if (!t.second) {  // a row of dA per lane
           uint16_t *dst = reinterpret_cast<uint16_t *>(a.dA) +
                           (static_cast<int64_t>(t.group) * a.K + base + lane) * a.r + c0;

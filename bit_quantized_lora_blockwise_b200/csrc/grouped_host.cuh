@@ -218,7 +218,7 @@ qlora_status run_gradients(const GradientArgs &a, int64_t units, int sms, cudaSt
   return run_gradients_bn<256, DROP>(a, units, sms, st);
 }
 
-// dA_e = (M o X_e)^T gs_e and dB_e = s xa_e^T dY_e, every expert's in one
+// dA_e = factor (M o X_e)^T gs_e and dB_e = s xa_e^T dY_e, every expert's in one
 // launch: over persistent CTAs (`keep`: the mask's bits, which dX left), else
 // with each tile's tokens split over a cluster.
 qlora_status grouped_adapter_grads(const void *X, const void *dY, const void *gs, const void *xa, const GroupedShape &s,
@@ -234,6 +234,7 @@ qlora_status grouped_adapter_grads(const void *X, const void *dY, const void *gs
       return QLORA_ERR_CUDA;
     a.dA = dA;
     a.dB = dB;
+    a.a_scale = drop.factor;
     a.b_scale = b_scale;
     a.K = static_cast<int>(s.K);
     a.N = static_cast<int>(s.N);
@@ -256,7 +257,7 @@ qlora_status grouped_adapter_grads(const void *X, const void *dY, const void *gs
     return QLORA_ERR_CUDA;
   A.out = dA;
   A.out_ld = s.r;
-  A.out_scale = 1.0f;
+  A.out_scale = drop.factor;
   A.rows = static_cast<int>(s.K);
   A.cols = s.r;
   B.out = dB;
@@ -376,15 +377,15 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
   const float scl = alpha / static_cast<float>(s.r);
   qlora_status st = QLORA_OK;
 
-  // 1) XA where it was not saved, and Gs = s dY B^T times the dropout factor
-  //    (dX and dA mask it, nothing else reads it), whose launch zeroes the
-  //    counters
+  // 1) XA where it was not saved, and Gs = s dY B^T, whose launch zeroes the
+  //    counters. (The dropout factor of dX and dA multiplies their fp32 sums:
+  //    in Gs it would cost fp16 that much of its range.)
   if (XA == nullptr) {
     st = grouped_rows(SK_XA, X, A, s, g, drop, xa_ws, drop.factor, nullptr, 0.0f, nullptr, 0, cs);
     if (st != QLORA_OK) return st;
     XA = xa_ws;
   }
-  st = grouped_rows(SK_G, dY, B, s, g, drop, gs, scl * drop.factor, nullptr, 0.0f, counters, p.counters, cs);
+  st = grouped_rows(SK_G, dY, B, s, g, drop, gs, scl, nullptr, 0.0f, counters, p.counters, cs);
   if (st != QLORA_OK) return st;
 
   // 2) dX
