@@ -39,10 +39,6 @@ struct AdamwHyper {
   int f16;         // 16-bit type of param and grad (else bf16)
 };
 
-__device__ __forceinline__ float from_16(uint16_t h, bool f16) {
-  return f16 ? __half2float(__ushort_as_half(h)) : __bfloat162float(__ushort_as_bfloat16(h));
-}
-
 // master, m, v: fp32 [total] each (managed memory). Element i of the state
 // belongs to the segment whose [offset[s], offset[s+1]) holds it.
 __global__ void __launch_bounds__(256) adamw_kernel(const AdamwSegs segs, float *__restrict__ master,

@@ -1,7 +1,7 @@
 // Adapter gradients of many experts in one persistent launch:
 //   dA_e = f (M o X_e)^T Gs_e   [K, r],    dB_e = s (XA_e^T dY_e)   [r, N]
-// (M, f: the dropout mask and factor, 1 without dropout), each the product over the
-// expert's tokens alone. skinny_kernel computes the same sums with one
+// (M, f: the dropout mask and factor, 1 without dropout), each the product over
+// the expert's tokens alone. skinny_kernel computes the same sums with one
 // cluster per tile, split over the tokens; with more tiles than resident CTAs
 // its cost is the CTA itself (tables, TMEM, first copies, shared-memory
 // reduction: some 10 us), not the sums. Here two CTAs per SM run over the
@@ -15,6 +15,15 @@
 // operands to zero in shared memory before the MMAs read them, so not even a
 // NaN there can enter. An expert without tokens has no units: its gradients
 // are set to zero by warp 3 of all CTAs.
+//
+// Gs is s dY B^T in two 16-bit parts (ptx.cuh), so that dA carries its own
+// rounding and none of G's: in one part dA's error was 1.4 times what its
+// rounding alone makes, and in fp16 a G below 2^-14 (B starts at zero) lost its
+// bits though dA, summed over the tokens, was in range. The parts lie side by
+// side in a stage and in TMEM: one MMA of twice the columns, joined at the
+// readout. (Backward of 8192 rows over 8 experts of 4096 x 11008 with dropout:
+// 807-828 us, 797-818 with G in one part.) A unit has at most 128 ranks; of more, a row tile's units follow one
+// another, so that the second finds its tokens in L2.
 //
 // Dropout: dX, the launch before this one, evaluates the same mask and leaves
 // its keep bits in the workspace (T K / 8 bytes). The units of dB come first:
@@ -39,7 +48,7 @@
 namespace qlora {
 
 struct GradientArgs {
-  CUtensorMap tm_x, tm_gs;   // X [T, K], Gs [T, r]: 64 x 64 boxes
+  CUtensorMap tm_x, tm_gs, tm_gs2;  // X [T, K], Gs [T, r] and its second part: 64 x 64 boxes
   CUtensorMap tm_dy, tm_xa;  // dY [T, N], XA [T, r]
   void *dA, *dB;             // [E, K, r], [E, r, N], 16-bit
   float a_scale, b_scale;    // f, s
@@ -103,7 +112,7 @@ template <int BN_, int STAGES_, bool DROP_>
 struct GradientCfg {
   static constexpr int BN = BN_, STAGES = STAGES_;
   static constexpr bool DROP = DROP_;
-  static constexpr int A_BYTES = 128 * 64 * 2, B_BYTES = BN_ * 64 * 2, STAGE = A_BYTES + B_BYTES;
+  static constexpr int A_BYTES = 128 * 64 * 2, PART = BN_ * 64 * 2, STAGE = A_BYTES + 2 * PART;
   static constexpr int OFF_BAR = STAGES_ * STAGE;
   static constexpr int UNITS = 4;  // ring of the CTA's units
   // full[S] empty[S] ready[S] tmem_full[2] tmem_empty[2] landed tail drain unit_full[U] unit_empty[U]
@@ -118,9 +127,9 @@ struct GradientCfg {
   static constexpr int SMEM_BYTES = OFF_CLASSES + kSizeClasses * 4;
   static constexpr int UNIT_READERS = DROP_ ? 14 : 6;  // MMA, tails, readout (4), mask (8)
   static constexpr int THREADS = DROP_ ? 512 : 256;
-  static constexpr uint32_t TMEM_COLS = 2 * BN_;
+  static constexpr uint32_t TMEM_COLS = 4 * BN_;  // two accumulators of two parts
   static constexpr int PER_SM = SMEM_BYTES <= 113 * 1024 ? 2 : 1;
-  static_assert(BN_ == 64 || BN_ == 128 || BN_ == 256, "rank tile");
+  static_assert(BN_ == 64 || BN_ == 128, "ranks of a unit");
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 };
 
@@ -184,11 +193,12 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
 
-  const int ta = (a.K + 127) / 128, tb = (a.N + 127) / 128;
+  const int nc = (a.r + C::BN - 1) / C::BN;  // units of a row tile
+  const int ta = (a.K + 127) / 128 * nc, tb = (a.N + 127) / 128 * nc;
   const int some = *s_some, nb = some * tb, units = nb + some * ta;
   struct Unit {
     bool second;  // dB
-    int group, row0, tok0, ntok, nk;  // nk > 0
+    int group, row0, rank0, tok0, ntok, nk;  // nk > 0
   };
   auto unit_at = [&](int u) {
     Unit t;
@@ -196,7 +206,9 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
     const int v = t.second ? u : u - nb, per = t.second ? tb : ta;
     const int at = v / per;
     t.group = s_order[at];
-    t.row0 = (v - at * per) * 128;
+    const int w = v - at * per, tile = w / nc;
+    t.row0 = tile * 128;
+    t.rank0 = (w - tile * nc) * C::BN;
     t.tok0 = gt.first[t.group];
     t.ntok = gt.first[t.group + 1] - t.tok0;
     t.nk = (t.ntok + 63) / 64;
@@ -247,11 +259,17 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
           const int s = it % C::STAGES, tok = t.tok0 + j * 64;
           if (!mbar_wait(empty_bar(s), ((it / C::STAGES) & 1u) ^ 1u, s_abort)) { ok = false; break; }
           const uint32_t dst = sbase + s * C::STAGE;
-          mbar_arrive_expect_tx(full_bar(s), C::STAGE);
+          mbar_arrive_expect_tx(full_bar(s), t.second ? C::A_BYTES + C::PART : C::STAGE);
           tma_load_2d(dst, ma, full_bar(s), t.row0, tok);
           tma_load_2d(dst + 8192, ma, full_bar(s), t.row0 + 64, tok);
 #pragma unroll
-          for (int c = 0; c < C::BN / 64; ++c) tma_load_2d(dst + C::A_BYTES + c * 8192, mb, full_bar(s), c * 64, tok);
+          for (int c = 0; c < C::BN / 64; ++c)
+            tma_load_2d(dst + C::A_BYTES + c * 8192, mb, full_bar(s), t.rank0 + c * 64, tok);
+          if (!t.second) {
+#pragma unroll
+            for (int c = 0; c < C::BN / 64; ++c)
+              tma_load_2d(dst + C::A_BYTES + C::PART + c * 8192, &a.tm_gs2, full_bar(s), t.rank0 + c * 64, tok);
+          }
         }
         u = static_cast<int>(gridDim.x + atomicAdd(a.counter, 1u));
       }
@@ -268,12 +286,14 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
     __syncwarp();
   } else if (warp == 1) {
     if (elect_one()) {
-      const uint32_t idesc = idesc_dtype(make_idesc_bf16(128, C::BN, 1, 1), a.f16);
+      const uint32_t id_one = idesc_dtype(make_idesc_bf16(128, C::BN, 1, 1), a.f16);
+      const uint32_t id_two = idesc_dtype(make_idesc_bf16(128, 2 * C::BN, 1, 1), a.f16);
       uint32_t it = 0, tails = 0;
       bool ok = true;
       for (uint32_t k = 0; ok && take_thread(k, t); ++k) {
         wait_dx(t);
         const int b = k & 1u;
+        const uint32_t idesc = t.second ? id_one : id_two;
         if (!mbar_wait(tmem_empty(b), ((k >> 1) & 1u) ^ 1u, s_abort)) { ok = false; break; }
         tc_fence_after();
         for (int j = 0; j < t.nk; ++j, ++it) {
@@ -288,7 +308,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
           const uint32_t ad = sbase + s * C::STAGE, bd = ad + C::A_BYTES;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_ss(tmem_base + b * C::BN, smem_desc_sw128(ad + kk * 2048, 8192, 1024),
+            tc_mma_ss(tmem_base + b * 2 * C::BN, smem_desc_sw128(ad + kk * 2048, 8192, 1024),
                       smem_desc_sw128(bd + kk * 2048, 8192, 1024), idesc, (j > 0 || kk > 0) ? 1u : 0u);
           tc_commit(empty_bar(s));
         }
@@ -318,7 +338,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
       ++tails;
       uint8_t *stage = smem + (it - 1) % C::STAGES * C::STAGE;
       const int first = rows * 8, per = 512 - first;  // 16-byte pieces of a chunk
-      for (int i = lane; i < per * (2 + C::BN / 64); i += 32) {
+      for (int i = lane; i < per * (2 + C::BN / 64 * (t.second ? 1 : 2)); i += 32) {
         const int c = i / per, o = first + i - c * per;
         *reinterpret_cast<uint4 *>(stage + c * 8192 + o * 16) = make_uint4(0u, 0u, 0u, 0u);
       }
@@ -329,6 +349,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
   } else if (warp >= 4 && warp < 8) {
     const int q = warp - 4;
     const bool f16 = a.f16 != 0;
+    const float inv = 1.0f / part_scale(f16);  // (a power of two)
     for (uint32_t k = 0; take_warp(k, t); ++k) {
       const int b = k & 1u;
       const float scale = t.second ? a.b_scale : a.a_scale;
@@ -337,22 +358,33 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
       tc_fence_after();
       const int base = t.row0 + q * 32;  // K and N are multiples of 64: 32 rows or none
 #pragma unroll 1
-      for (int c0 = 0; c0 < a.r && base < (t.second ? a.N : a.K); c0 += 32) {
-        uint32_t w[32];
-        tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * C::BN + c0, w);
-        float v[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]) * scale;
-        if (!t.second) {  // a row of dA per lane
+      for (int ch = 0; ch < C::BN && t.rank0 + ch < a.r && base < (t.second ? a.N : a.K); ch += 32) {
+        const int c0 = t.rank0 + ch;
+        const uint32_t tcol = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * 2 * C::BN + ch;
+        if (!t.second) {  // a row of dA per lane, 16 columns of both parts at a time
           uint16_t *dst = reinterpret_cast<uint16_t *>(a.dA) +
                           (static_cast<int64_t>(t.group) * a.K + base + lane) * a.r + c0;
+#pragma unroll 1
+          for (int h = 0; h < 32 && c0 + h < a.r; h += 16) {
+            uint32_t w[16], w2[16];
+            tmem_ld_32x32b_x16(tcol + h, w);
+            tmem_ld_32x32b_x16(tcol + C::BN + h, w2);
+            float v[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (c0 + 8 * i < a.r)
-              *reinterpret_cast<uint4 *>(dst + 8 * i) =
-                  make_uint4(pack_16x2(v[8 * i], v[8 * i + 1], f16), pack_16x2(v[8 * i + 2], v[8 * i + 3], f16),
-                             pack_16x2(v[8 * i + 4], v[8 * i + 5], f16), pack_16x2(v[8 * i + 6], v[8 * i + 7], f16));
+            for (int j = 0; j < 16; ++j) v[j] = join_parts(w[j], w2[j], inv) * scale;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (c0 + h + 8 * i < a.r)
+                *reinterpret_cast<uint4 *>(dst + h + 8 * i) =
+                    make_uint4(pack_16x2(v[8 * i], v[8 * i + 1], f16), pack_16x2(v[8 * i + 2], v[8 * i + 3], f16),
+                               pack_16x2(v[8 * i + 4], v[8 * i + 5], f16), pack_16x2(v[8 * i + 6], v[8 * i + 7], f16));
+          }
         } else {  // dB is stored along N
+          uint32_t w[32];
+          tmem_ld_32x32b_x32(tcol, w);
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]) * scale;
           uint4 out[4];
           rows_to_columns(v, lane, f16, out);
 #pragma unroll

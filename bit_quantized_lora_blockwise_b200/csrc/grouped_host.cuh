@@ -81,8 +81,9 @@ bool persistent_gradients(const GroupedShape &s, int sms) {
   return s.E * (cdiv(s.K, 128) + cdiv(s.N, 128)) > (s.r <= 128 ? 2 : 1) * static_cast<int64_t>(sms);
 }
 
-// [counters][16-bit T x r][16-bit T x r (backward)][fp32 partials][keep bits T x
-// K / 8 (backward with dropout, for gradient_kernel)]
+// [counters][16-bit T x r: s XA, or Gs][backward: 16-bit T x r twice, Gs' second
+// part and XA][fp32 partials][keep bits T x K / 8 (backward with dropout, for
+// gradient_kernel)]
 struct GroupedWs {
   size_t counters, tr, part, keep, total;
 };
@@ -92,7 +93,7 @@ GroupedWs grouped_ws(const GroupedShape &s, int64_t ncounters, size_t part, bool
   w.tr = align256(static_cast<size_t>(s.T) * s.r * 2);
   w.part = part;
   w.keep = backward && s.drop && persistent_gradients(s, sms) ? align256(static_cast<size_t>(s.T) * (s.K / 8)) : 0;
-  w.total = w.counters + (backward ? 2 : 1) * w.tr + w.part + w.keep;
+  w.total = w.counters + (backward ? 3 : 1) * w.tr + w.part + w.keep;
   return w;
 }
 
@@ -149,7 +150,8 @@ bool map_experts_3d(CUtensorMap *map, const void *p, int64_t inner, int64_t oute
 }
 
 // out[T, r] = scale * rows . adapter_e: X A (kind SK_XA; with dropout (M o X)
-// A) or dY B^T (SK_G), optionally a second copy with another scale.
+// A) or dY B^T (SK_G). out2: for X A optionally a second copy with another
+// scale, for dY B^T the second part of what out rounds.
 qlora_status grouped_rows(SkinnyKind kind, const void *rows, const void *adapter, const GroupedShape &s,
                           const GroupArgs &g, const DropoutArgs &drop, void *out, float scale, void *out2, float scale2,
                           unsigned int *zero_words, int64_t nzero, cudaStream_t st) {
@@ -174,6 +176,7 @@ qlora_status grouped_rows(SkinnyKind kind, const void *rows, const void *adapter
   P.out2 = out2;
   P.out2_ld = s.r;
   P.out2_scale = scale2;
+  P.rest = kind == SK_G ? 1 : 0;
   P.rows = static_cast<int>(s.T);
   P.cols = s.r;
   P.kblocks = static_cast<int>(kdim / 64);
@@ -194,7 +197,7 @@ qlora_status grouped_rows(SkinnyKind kind, const void *rows, const void *adapter
 
 template <int BN, bool DROP>
 qlora_status run_gradients_bn(const GradientArgs &a, int64_t units, int sms, cudaStream_t st) {
-  using C = GradientCfg<BN, skinny_stages(BN), DROP>;
+  using C = GradientCfg<BN, BN == 64 ? 3 : 4, DROP>;  // 96 KB of ring, two CTAs an SM; or 192 KB
   static std::once_flag once[kMaxDevices];
   static cudaError_t err[kMaxDevices];
   int dev = 0;
@@ -212,25 +215,24 @@ qlora_status run_gradients_bn(const GradientArgs &a, int64_t units, int sms, cud
 
 template <bool DROP>
 qlora_status run_gradients(const GradientArgs &a, int64_t units, int sms, cudaStream_t st) {
-  const int bn = rank_tile(a.r);
-  if (bn == 64) return run_gradients_bn<64, DROP>(a, units, sms, st);
-  if (bn == 128) return run_gradients_bn<128, DROP>(a, units, sms, st);
-  return run_gradients_bn<256, DROP>(a, units, sms, st);
+  if (a.r <= 64) return run_gradients_bn<64, DROP>(a, units, sms, st);
+  return run_gradients_bn<128, DROP>(a, units * cdiv(a.r, 128), sms, st);
 }
 
-// dA_e = factor (M o X_e)^T gs_e and dB_e = s xa_e^T dY_e, every expert's in one
+// dA_e = factor (M o X_e)^T Gs_e (gs, gs2: its two parts) and dB_e = s xa_e^T dY_e, every expert's in one
 // launch: over persistent CTAs (`keep`: the mask's bits, which dX left), else
 // with each tile's tokens split over a cluster.
-qlora_status grouped_adapter_grads(const void *X, const void *dY, const void *gs, const void *xa, const GroupedShape &s,
-                                   const GroupArgs &g, const DropoutArgs &drop, const uint32_t *keep,
-                                   unsigned int *unit_counter, void *dA, void *dB, float b_scale, int sms,
-                                   cudaStream_t st) {
+qlora_status grouped_adapter_grads(const void *X, const void *dY, const void *gs, const void *gs2, const void *xa,
+                                   const GroupedShape &s, const GroupArgs &g, const DropoutArgs &drop,
+                                   const uint32_t *keep, unsigned int *unit_counter, void *dA, void *dB,
+                                   float b_scale, int sms, cudaStream_t st) {
   const int64_t ta = s.E * cdiv(s.K, 128), tb = s.E * cdiv(s.N, 128);
   if (persistent_gradients(s, sms)) {
     GradientArgs a;
     std::memset(&a, 0, sizeof a);
     if (!map_mnmajor(&a.tm_x, X, s.K, s.T) || !map_mnmajor(&a.tm_gs, gs, s.r, s.T) ||
-        !map_mnmajor(&a.tm_dy, dY, s.N, s.T) || !map_mnmajor(&a.tm_xa, xa, s.r, s.T))
+        !map_mnmajor(&a.tm_gs2, gs2, s.r, s.T) || !map_mnmajor(&a.tm_dy, dY, s.N, s.T) ||
+        !map_mnmajor(&a.tm_xa, xa, s.r, s.T))
       return QLORA_ERR_CUDA;
     a.dA = dA;
     a.dB = dB;
@@ -253,8 +255,11 @@ qlora_status grouped_adapter_grads(const void *X, const void *dY, const void *gs
   std::memset(&a, 0, sizeof a);
   SkinnyProblem &A = a.prob[0], &B = a.prob[1];
   if (!map_mnmajor(&A.tm_a, X, s.K, s.T) || !map_mnmajor(&A.tm_b, gs, s.r, s.T) ||
-      !map_mnmajor(&B.tm_a, dY, s.N, s.T) || !map_mnmajor(&B.tm_b, xa, s.r, s.T))
+      !map_mnmajor(&A.tm_b2, gs2, s.r, s.T) || !map_mnmajor(&B.tm_a, dY, s.N, s.T) ||
+      !map_mnmajor(&B.tm_b, xa, s.r, s.T))
     return QLORA_ERR_CUDA;
+  A.parts = 2;
+  B.parts = 1;
   A.out = dA;
   A.out_ld = s.r;
   A.out_scale = drop.factor;
@@ -370,22 +375,24 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   unsigned int *counters = reinterpret_cast<unsigned int *>(ws);
   void *gs = ws + w.counters;
-  void *xa_ws = ws + w.counters + w.tr;
-  float *part = reinterpret_cast<float *>(ws + w.counters + 2 * w.tr);
-  uint32_t *keep = w.keep > 0 ? reinterpret_cast<uint32_t *>(ws + w.counters + 2 * w.tr + w.part) : nullptr;
+  void *gs2 = ws + w.counters + w.tr;
+  void *xa_ws = ws + w.counters + 2 * w.tr;
+  float *part = reinterpret_cast<float *>(ws + w.counters + 3 * w.tr);
+  uint32_t *keep = w.keep > 0 ? reinterpret_cast<uint32_t *>(ws + w.counters + 3 * w.tr + w.part) : nullptr;
   const GroupArgs g{offsets, static_cast<int>(s.E), static_cast<int>(s.T)};
   const float scl = alpha / static_cast<float>(s.r);
   qlora_status st = QLORA_OK;
 
-  // 1) XA where it was not saved, and Gs = s dY B^T, whose launch zeroes the
-  //    counters. (The dropout factor of dX and dA multiplies their fp32 sums:
-  //    in Gs it would cost fp16 that much of its range.)
+  // 1) XA where it was not saved, and Gs = s dY B^T in two parts (dA reads
+  //    both, dX the first), whose launch zeroes the counters. (The dropout
+  //    factor of dX and dA multiplies their fp32 sums: in Gs it would cost fp16
+  //    that much of its range.)
   if (XA == nullptr) {
     st = grouped_rows(SK_XA, X, A, s, g, drop, xa_ws, drop.factor, nullptr, 0.0f, nullptr, 0, cs);
     if (st != QLORA_OK) return st;
     XA = xa_ws;
   }
-  st = grouped_rows(SK_G, dY, B, s, g, drop, gs, scl, nullptr, 0.0f, counters, p.counters, cs);
+  st = grouped_rows(SK_G, dY, B, s, g, drop, gs, scl, gs2, scl, counters, p.counters, cs);
   if (st != QLORA_OK) return st;
 
   // 2) dX
@@ -410,5 +417,5 @@ qlora_status grouped_bwd(const uint8_t *packed, const uint8_t *q, const float *s
   // 3) dA and dB "late", as in the dense backward: every operand but the keep
   //    bits (whose readers wait for them) is complete when this launch starts,
   //    and dX is neither read nor written by it
-  return grouped_adapter_grads(X, dY, gs, XA, s, g, drop, keep, counters + 2 * p.slots, dA, dB, scl, sms, cs);
+  return grouped_adapter_grads(X, dY, gs, gs2, XA, s, g, drop, keep, counters + 2 * p.slots, dA, dB, scl, sms, cs);
 }

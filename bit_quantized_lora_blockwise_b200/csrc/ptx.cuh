@@ -548,6 +548,27 @@ __device__ __forceinline__ uint16_t to_16(float v, bool f16) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+__device__ __forceinline__ float from_16(uint16_t v, bool f16) {
+  return f16 ? __half2float(__ushort_as_half(v)) : __bfloat162float(__ushort_as_bfloat16(v));
+}
+
+// A value in two 16-bit parts: v ~ hi + lo / c with hi = v rounded and lo what
+// that rounds away, times c = 2^11 (fp16) or 2^8 (bf16). c is the largest
+// power of two for which lo never exceeds hi's binade, so lo cannot overflow,
+// and in fp16 it stays a normal number down to |v| of 2^-25, 2^-14 times
+// smaller than hi does. An infinite or NaN hi has no rest: lo = 0.
+__host__ __device__ __forceinline__ float part_scale(bool f16) { return f16 ? 2048.0f : 256.0f; }
+__device__ __forceinline__ uint16_t second_part(float v, uint16_t hi, bool f16) {
+  const float h = from_16(hi, f16);
+  return isfinite(h) ? to_16((v - h) * part_scale(f16), f16) : static_cast<uint16_t>(0);
+}
+// The sum of two products with the parts, accumulators as bits (inv: 1 /
+// part_scale). One that is not finite stays what the first part made it: an
+// infinite factor times a second part of 0 says nothing.
+__device__ __forceinline__ float join_parts(uint32_t hi, uint32_t lo, float inv) {
+  const float h = __uint_as_float(hi);
+  return isfinite(h) ? fmaf(__uint_as_float(lo), inv, h) : h;
+}
 
 // ------------------------------------------------ 32 x 32 warp transposes --
 // A warp holds 32 rows (one per lane) of 32 columns and stores them column by

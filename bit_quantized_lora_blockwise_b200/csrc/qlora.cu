@@ -456,13 +456,16 @@ int rank_tile(int r) { return r <= 64 ? 64 : (r <= 128 ? 128 : 256); }
 // (r <= 128) keep two CTAs on an SM; r <= 256 uses 4 stages of 48 KB.
 // (Rings of about 192 KB per CTA, one CTA per SM, measured no faster.)
 constexpr int skinny_stages(int bn) { return bn == 64 ? 4 : (bn == 128 ? 3 : 4); }
+// With two parts of G beside X (adapter gradients of the grouped calls): 3
+// stages of 32 KB or 2 of 48 KB, two CTAs on an SM; 2 of 80 KB for r <= 256.
+constexpr int skinny_stages_two(int bn) { return bn == 64 ? 3 : 2; }
 
 // One skinny-GEMM variant: its shared-memory opt-in and how many clusters
 // of 2, 4 and 8 CTAs can be resident at once (asked of the runtime once per
 // device).
 template <int BN, bool AMN, bool BMN, bool GROUPED = false, bool DROP = false>
 struct SkinnyVariant {
-  using C = SkinnyCfg<BN, AMN, BMN, skinny_stages(BN), GROUPED, DROP>;
+  using C = SkinnyCfg<BN, AMN, BMN, GROUPED && AMN ? skinny_stages_two(BN) : skinny_stages(BN), GROUPED, DROP>;
   static qlora_status prepare(int (&max_clusters)[4], int *per_sm) {
     static std::once_flag once[kMaxDevices];
     static cudaError_t err[kMaxDevices];

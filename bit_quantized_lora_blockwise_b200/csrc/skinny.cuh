@@ -26,7 +26,11 @@
 // 64-token block may reach into the next expert's rows: warp 2 sets those
 // rows of both operands to zero in shared memory before the MMAs read them,
 // so that not even a NaN there can enter this expert's gradient. An expert
-// without tokens gets zeros.
+// without tokens gets zeros. dA takes G in two 16-bit parts, which the dY B^T
+// launch writes (ptx.cuh; the reasons are in gradients.cuh): the second part's
+// columns follow the first's in a stage and in TMEM, and the readout joins
+// them. (Backward of 2048 rows, 11008 x 4096 with dropout: 187 us, 184 with G
+// in one part.)
 //
 // Adapter dropout (DROP = true): the product reads M o X in place of X (kept
 // elements as they are; the factor is in the output's scale). X never makes
@@ -50,6 +54,7 @@ namespace qlora {
 struct SkinnyProblem {
   CUtensorMap tm_a;  // A operand: K-major box {64, 128} or MN-major 64x64 chunks
   CUtensorMap tm_b;  // B operand: K-major box {64, BN} or MN-major 64x64 chunks
+  CUtensorMap tm_b2;  // TWO_PART, parts == 2: the B operand's second part
   void *out;         // bf16 [rows, cols] (ld out_ld) or transposed [cols, rows]
   void *out2;        // optional second output, same layout
   int64_t out_ld, out2_ld;
@@ -59,6 +64,8 @@ struct SkinnyProblem {
   int cols;     // r
   int kblocks;  // 64-deep K blocks in total
   int masked;   // DROP: the A operand is taken through the mask (X; not dY)
+  int parts;    // TWO_PART: 16-bit parts of the B operand (2: Gs; else XA, in one)
+  int rest;     // GROUPED: out2 (same scale) holds the second part of what out rounds: G, for dA
 };
 
 struct SkinnyArgs {
@@ -88,7 +95,10 @@ struct SkinnyCfg {
   static constexpr bool A_MN = A_MN_, B_MN = B_MN_;
   static_assert(BN_ % 64 == 0 && BN_ <= 256, "rank tile");
   static constexpr int A_BYTES = 128 * 64 * 2;
-  static constexpr int B_BYTES = BN_ * 64 * 2;
+  // dA's G comes in two 16-bit parts (ptx.cuh), side by side in a stage and in TMEM
+  static constexpr bool TWO_PART = GROUPED_ && A_MN_;
+  static constexpr int PART_BYTES = BN_ * 64 * 2;
+  static constexpr int B_BYTES = PART_BYTES * (TWO_PART ? 2 : 1);
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = STAGES_ * A_BYTES;
   static constexpr int OFF_BAR = OFF_B + STAGES_ * B_BYTES;
@@ -98,11 +108,11 @@ struct SkinnyCfg {
   static constexpr int OFF_GROUPS = OFF_MISC + 16;
   static constexpr int SMEM_BYTES = OFF_GROUPS + (GROUPED_ ? kGroupTableBytes : 0);
   static constexpr int THREADS = DROP_ ? 384 : 256;  // DROP: warps 8-11 mask beside warps 4-7
-  static constexpr uint32_t TMEM_COLS = BN_ <= 64 ? 64 : (BN_ <= 128 ? 128 : 256);
+  static constexpr uint32_t TMEM_COLS = (BN_ <= 64 ? 64 : (BN_ <= 128 ? 128 : 256)) * (TWO_PART ? 2 : 1);
   static constexpr int PART_LD = BN_ + 4;  // fp32 per partial row (16-byte pad against bank conflicts)
   static_assert(128 * PART_LD * 4 <= OFF_BAR, "the partial reuses the ring");
   static_assert(SMEM_BYTES <= (BN_ <= 128 ? 113 * 1024 : 232448), "shared memory per CTA: two on an SM up to rank 128");
-  static constexpr uint32_t TX = A_BYTES + B_BYTES;
+  static constexpr uint32_t TX = A_BYTES + PART_BYTES;  // (and another PART_BYTES for a second part)
 };
 
 template <class C>
@@ -137,6 +147,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
   if (warp == 3 && lane == 0) {
     tma_prefetch_desc(&P.tm_a);
     tma_prefetch_desc(&P.tm_b);
+    if (C::TWO_PART && P.parts == 2) tma_prefetch_desc(&P.tm_b2);
   }
   if constexpr (C::GROUPED) {
     // late launches run on inputs that are complete when they start
@@ -202,7 +213,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
     const int kb = kb_begin + j;
     const uint32_t a_dst = sbase + C::OFF_A + s * C::A_BYTES;
     const uint32_t b_dst = sbase + C::OFF_B + s * C::B_BYTES;
-    mbar_arrive_expect_tx(full_bar(s), C::TX);
+    mbar_arrive_expect_tx(full_bar(s), C::TX + (C::TWO_PART && P.parts == 2 ? C::PART_BYTES : 0));
     if constexpr (C::GROUPED) {
       if (C::A_MN) {  // token rows of both operands from the expert's first one on
         const int tok = tok0 + kb * 64;
@@ -210,6 +221,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
         tma_load_2d(a_dst + 8192, &P.tm_a, full_bar(s), row0 + 64, tok);
 #pragma unroll
         for (int c = 0; c < C::BN / 64; ++c) tma_load_2d(b_dst + c * 8192, &P.tm_b, full_bar(s), c * 64, tok);
+        if (P.parts == 2) {
+#pragma unroll
+          for (int c = 0; c < C::BN / 64; ++c)
+            tma_load_2d(b_dst + C::PART_BYTES + c * 8192, &P.tm_b2, full_bar(s), c * 64, tok);
+        }
       } else {  // the expert's adapter: a slice of a 3-D map
         tma_load_2d(a_dst, &P.tm_a, full_bar(s), kb * 64, row0);
         if (C::B_MN) {
@@ -282,6 +298,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
           const uint64_t bd = C::B_MN ? smem_desc_sw128(b_addr + kk * 2048, 8192, 1024)
                                       : smem_desc_sw128(b_addr + kk * 32, 16, 1024);
           tc_mma_ss(tmem_base, ad, bd, idesc, (j > 0 || kk > 0) ? 1u : 0u);
+          if (C::TWO_PART && P.parts == 2)
+            tc_mma_ss(tmem_base + C::BN, ad, smem_desc_sw128(b_addr + C::PART_BYTES + kk * 2048, 8192, 1024), idesc,
+                      (j > 0 || kk > 0) ? 1u : 0u);
         }
         tc_commit(empty_bar(s));
       }
@@ -301,8 +320,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
       const int s = (nk - 1) % C::STAGES;
       if (warp_wait_all(landed_bar, 0, s_abort)) {
         const int first = tail_rows * 8, per = 512 - first;  // 16-byte pieces of a chunk
-        constexpr int NCH = 2 + C::BN / 64;
-        for (int i = lane; i < per * NCH; i += 32) {
+        const int nch = 2 + C::BN / 64 * (P.parts == 2 ? 2 : 1);
+        for (int i = lane; i < per * nch; i += 32) {
           const int c = i / per, o = first + i - c * per;
           uint8_t *chunk = c < 2 ? smem + C::OFF_A + s * C::A_BYTES + c * 8192
                                  : smem + C::OFF_B + s * C::B_BYTES + (c - 2) * 8192;
@@ -379,6 +398,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
 #pragma unroll
         for (int j = 0; j < 32; ++j) u[j] = 0u;
       }
+      if (C::TWO_PART && P.parts == 2 && ok && nk > 0) {
+        uint32_t w[32];
+        tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>((q & 3) * 32) << 16) + C::BN + ch * 32, w);
+        const float inv = 1.0f / part_scale(args.f16 != 0);  // (a power of two)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(join_parts(u[j], w[j], inv));
+      }
       float4 *dst = reinterpret_cast<float4 *>(part + lrow * C::PART_LD + ch * 32);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -441,8 +467,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) skinny_kernel(const __grid_cons
 #pragma unroll
           for (int e = 0; e < 4; ++e) dst[static_cast<int64_t>(c4 * 4 + e) * ld + row] = to_16(vv[e] * sc, f16);
         } else {
-          *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(row) * ld + c4 * 4) =
-              make_uint2(pack_16x2(vv[0] * sc, vv[1] * sc, f16), pack_16x2(vv[2] * sc, vv[3] * sc, f16));
+          uint2 w = make_uint2(pack_16x2(vv[0] * sc, vv[1] * sc, f16), pack_16x2(vv[2] * sc, vv[3] * sc, f16));
+          if (C::GROUPED && o && P.rest) {  // out2_scale is out_scale: what `out` rounded away
+            auto rest = [&](int e, uint32_t pair) {
+              return static_cast<uint32_t>(
+                  second_part(vv[e] * sc, static_cast<uint16_t>(e & 1 ? pair >> 16 : pair), f16));
+            };
+            w = make_uint2(rest(0, w.x) | rest(1, w.x) << 16, rest(2, w.y) | rest(3, w.y) << 16);
+          }
+          *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(row) * ld + c4 * 4) = w;
         }
       }
     }

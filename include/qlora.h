@@ -500,8 +500,10 @@ QLORA_API qlora_status qlora_dropout(const void *x, void *y, int64_t n, qlora_el
  *     be given: with many experts and rows a backward leaves the mask's bits
  *     there between its launches). Calls that may overlap on the device need
  *     a workspace each.
- * Accumulation is fp32; s X A and G are rounded to 16 bits before their
- * rank-r products, everything else once. Experts are isolated: a NaN or an
+ * Accumulation is fp32. s XA (XA = D(X) A) and, for dX, G are rounded to 16
+ * bits before their rank-r products; dA takes G in two 16-bit parts, which lose
+ * nothing that its own rounding keeps, down to |G| of 2^-25 in fp16. Everything
+ * else is rounded once; the dropout factor is applied in fp32. Experts are isolated: a NaN or an
  * infinity in one expert's rows or adapters reaches that expert's outputs
  * only.
  * Requires 1 <= E <= QLORA_MAX_EXPERTS, T >= 0 (T = 0: token pointers may be
