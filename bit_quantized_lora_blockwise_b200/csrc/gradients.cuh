@@ -22,8 +22,9 @@
 // bits though dA, summed over the tokens, was in range. The parts lie side by
 // side in a stage and in TMEM: one MMA of twice the columns, joined at the
 // readout. (Backward of 8192 rows over 8 experts of 4096 x 11008 with dropout:
-// 807-828 us, 797-818 with G in one part.) A unit has at most 128 ranks; of more, a row tile's units follow one
-// another, so that the second finds its tokens in L2.
+// 807-828 us, 797-818 with G in one part.) A unit has at most BN ranks of dA or
+// 2 BN of dB; of more, a row tile's units follow one another, so that the
+// second finds its tokens in L2.
 //
 // Dropout: dX, the launch before this one, evaluates the same mask and leaves
 // its keep bits in the workspace (T K / 8 bytes). The units of dB come first:
@@ -108,6 +109,13 @@ __device__ __forceinline__ int order_by_size(const GroupTable &gt, int groups, i
   return some;
 }
 
+// Units of a 128-row tile of dA and of dB.
+template <int BN>
+struct GradientUnits {
+  __host__ __device__ static constexpr int of_dA(int r) { return (r + BN - 1) / BN; }
+  __host__ __device__ static constexpr int of_dB(int r) { return (r + 2 * BN - 1) / (2 * BN); }
+};
+
 template <int BN_, int STAGES_, bool DROP_>
 struct GradientCfg {
   static constexpr int BN = BN_, STAGES = STAGES_;
@@ -129,7 +137,7 @@ struct GradientCfg {
   static constexpr int THREADS = DROP_ ? 512 : 256;
   static constexpr uint32_t TMEM_COLS = 4 * BN_;  // two accumulators of two parts
   static constexpr int PER_SM = SMEM_BYTES <= 113 * 1024 ? 2 : 1;
-  static_assert(BN_ == 64 || BN_ == 128, "ranks of a unit");
+  static_assert(BN_ == 64 || BN_ == 128, "ranks of a unit of dA");
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 };
 
@@ -193,12 +201,13 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
 
-  const int nc = (a.r + C::BN - 1) / C::BN;  // units of a row tile
-  const int ta = (a.K + 127) / 128 * nc, tb = (a.N + 127) / 128 * nc;
+  const int na = GradientUnits<C::BN>::of_dA(a.r), nb1 = GradientUnits<C::BN>::of_dB(a.r);
+  const int ta = (a.K + 127) / 128 * na, tb = (a.N + 127) / 128 * nb1;
   const int some = *s_some, nb = some * tb, units = nb + some * ta;
   struct Unit {
     bool second;  // dB
     int group, row0, rank0, tok0, ntok, nk;  // nk > 0
+    bool wide;    // both halves of the stage's B operand: two parts of BN ranks, or 2 BN ranks
   };
   auto unit_at = [&](int u) {
     Unit t;
@@ -206,9 +215,10 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
     const int v = t.second ? u : u - nb, per = t.second ? tb : ta;
     const int at = v / per;
     t.group = s_order[at];
-    const int w = v - at * per, tile = w / nc;
+    const int w = v - at * per, n = t.second ? nb1 : na, tile = w / n;
     t.row0 = tile * 128;
-    t.rank0 = (w - tile * nc) * C::BN;
+    t.rank0 = (w - tile * n) * (t.second ? 2 * C::BN : C::BN);
+    t.wide = !t.second || a.r - t.rank0 > C::BN;
     t.tok0 = gt.first[t.group];
     t.ntok = gt.first[t.group + 1] - t.tok0;
     t.nk = (t.ntok + 63) / 64;
@@ -255,20 +265,22 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
         t = unit_at(u);
         wait_dx(t);
         const CUtensorMap *ma = t.second ? &a.tm_dy : &a.tm_x, *mb = t.second ? &a.tm_xa : &a.tm_gs;
+        const CUtensorMap *mb2 = t.second ? &a.tm_xa : &a.tm_gs2;
+        const int rank2 = t.second ? t.rank0 + C::BN : t.rank0;
         for (int j = 0; j < t.nk; ++j, ++it) {
           const int s = it % C::STAGES, tok = t.tok0 + j * 64;
           if (!mbar_wait(empty_bar(s), ((it / C::STAGES) & 1u) ^ 1u, s_abort)) { ok = false; break; }
           const uint32_t dst = sbase + s * C::STAGE;
-          mbar_arrive_expect_tx(full_bar(s), t.second ? C::A_BYTES + C::PART : C::STAGE);
+          mbar_arrive_expect_tx(full_bar(s), t.wide ? C::STAGE : C::STAGE - C::PART);
           tma_load_2d(dst, ma, full_bar(s), t.row0, tok);
           tma_load_2d(dst + 8192, ma, full_bar(s), t.row0 + 64, tok);
 #pragma unroll
           for (int c = 0; c < C::BN / 64; ++c)
             tma_load_2d(dst + C::A_BYTES + c * 8192, mb, full_bar(s), t.rank0 + c * 64, tok);
-          if (!t.second) {
+          if (t.wide) {
 #pragma unroll
             for (int c = 0; c < C::BN / 64; ++c)
-              tma_load_2d(dst + C::A_BYTES + C::PART + c * 8192, &a.tm_gs2, full_bar(s), t.rank0 + c * 64, tok);
+              tma_load_2d(dst + C::A_BYTES + C::PART + c * 8192, mb2, full_bar(s), rank2 + c * 64, tok);
           }
         }
         u = static_cast<int>(gridDim.x + atomicAdd(a.counter, 1u));
@@ -293,7 +305,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
       for (uint32_t k = 0; ok && take_thread(k, t); ++k) {
         wait_dx(t);
         const int b = k & 1u;
-        const uint32_t idesc = t.second ? id_one : id_two;
+        const uint32_t idesc = t.wide ? id_two : id_one;
         if (!mbar_wait(tmem_empty(b), ((k >> 1) & 1u) ^ 1u, s_abort)) { ok = false; break; }
         tc_fence_after();
         for (int j = 0; j < t.nk; ++j, ++it) {
@@ -338,7 +350,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
       ++tails;
       uint8_t *stage = smem + (it - 1) % C::STAGES * C::STAGE;
       const int first = rows * 8, per = 512 - first;  // 16-byte pieces of a chunk
-      for (int i = lane; i < per * (2 + C::BN / 64 * (t.second ? 1 : 2)); i += 32) {
+      for (int i = lane; i < per * (2 + C::BN / 64 * (t.wide ? 2 : 1)); i += 32) {
         const int c = i / per, o = first + i - c * per;
         *reinterpret_cast<uint4 *>(stage + c * 8192 + o * 16) = make_uint4(0u, 0u, 0u, 0u);
       }
@@ -358,7 +370,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) gradient_kernel(const _
       tc_fence_after();
       const int base = t.row0 + q * 32;  // K and N are multiples of 64: 32 rows or none
 #pragma unroll 1
-      for (int ch = 0; ch < C::BN && t.rank0 + ch < a.r && base < (t.second ? a.N : a.K); ch += 32) {
+      for (int ch = 0; ch < (t.second ? 2 : 1) * C::BN && t.rank0 + ch < a.r && base < (t.second ? a.N : a.K); ch += 32) {
         const int c0 = t.rank0 + ch;
         const uint32_t tcol = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * 2 * C::BN + ch;
         if (!t.second) {  // a row of dA per lane, 16 columns of both parts at a time

@@ -554,9 +554,10 @@ __device__ __forceinline__ float from_16(uint16_t v, bool f16) {
 
 // A value in two 16-bit parts: v ~ hi + lo / c with hi = v rounded and lo what
 // that rounds away, times c = 2^11 (fp16) or 2^8 (bf16). c is the largest
-// power of two for which lo never exceeds hi's binade, so lo cannot overflow,
-// and in fp16 it stays a normal number down to |v| of 2^-25, 2^-14 times
-// smaller than hi does. An infinite or NaN hi has no rest: lo = 0.
+// power of two for which lo never exceeds hi's binade, so lo cannot overflow;
+// in fp16 the two hold v to 2^-36, which is half a unit of that type's last
+// place for |v| down to 2^-25 (hi alone: down to 2^-14). An infinite or NaN hi
+// has no rest: lo = 0.
 __host__ __device__ __forceinline__ float part_scale(bool f16) { return f16 ? 2048.0f : 256.0f; }
 __device__ __forceinline__ uint16_t second_part(float v, uint16_t hi, bool f16) {
   const float h = from_16(hi, f16);
