@@ -530,7 +530,8 @@ def dropout(x: torch.Tensor, drop: Dropout, out=None) -> torch.Tensor:
 
 def grouped_workspace_bytes(E: int, T: int, N: int, K: int, r: int, dropout: bool = False) -> int:
     """Scratch bytes of grouped_linear_fwd / grouped_linear_bwd (either), and,
-    with E = 1, of linear_fwd / linear_bwd with dropout. 0: shape refused."""
+    with E = 1, of linear_fwd / linear_bwd with dropout, on the current device.
+    0: shape refused."""
     return int(load().qlora_grouped_workspace_bytes(E, T, N, K, r, 1 if dropout else 0))
 
 
@@ -594,7 +595,8 @@ def _grouped_checks(packed, q, scale2, X, offsets, A, B, N, K, workspace, drop, 
     if offsets is not None:
         _need(offsets, "offsets", torch.int32, (E + 1,), dev)
     if workspace is None:
-        need = grouped_workspace_bytes(E, T, N, K, r, drop is not None)
+        with _on(dev):  # the size goes by the device's CTA slots
+            need = grouped_workspace_bytes(E, T, N, K, r, drop is not None)
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", torch.uint8, workspace.shape, dev)
     return E, T, r, dt, dev, workspace
