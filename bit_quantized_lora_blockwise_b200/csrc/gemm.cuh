@@ -159,8 +159,13 @@ struct GemmCfg {
   // but the code slots that their room costs starve the dequant warps.)
   static constexpr bool ONE_RING = BKB_ == 1 && SA_ == SB_;
   static_assert(NPW_ % 4 == 0 && NPW_ >= 4 && SP_ >= 2, "producer groups of 4 warps and a packed-code ring");
-  // (a 16-warp, 3-slot configuration timed out on B200: every producer group
-  // needs a slot of its own plus a spare, or the groups wait on each other)
+  // A group's next decoded-weight slot is NGROUPS further, wrapped once: the
+  // ring has no fewer slots than groups, and one more so that a group need not
+  // wait for the MMAs of its own last tile. (Three slots under four groups made
+  // the bounded waits run out on B200.) The packed-code ring may have fewer
+  // slots than groups: job j waits for codes, whose slot only jobs before j
+  // hold, and for a decoded-weight slot, which the MMAs of a job before j free,
+  // so the earliest job that is not done can always go on.
   static_assert(SA_ > NPW_ / 4, "dequantized-tile ring needs more slots than producer groups");
   static_assert(BN_ % 16 == 0 && BN_ >= 16 && BN_ <= 256 && B_ROWS % 8 == 0, "MMA N");
   static_assert(BKB_ >= 1 && BKB_ <= 4, "K blocks per token stage");

@@ -696,8 +696,8 @@ constexpr int64_t kTwoSubtileTokens = 1024;
 // (a 16 KB box), the 256-token fallback 1 (a 32 KB box).
 constexpr int single_bkb(int bn) { return bn == 32 ? 4 : 1; }
 
-// Resident pair slots for the fused GEMMs on this device (both variants have
-// the same shared memory and threads), 0 if the runtime reports none.
+// Resident pair slots that each of the fused GEMMs' pair variants has on this
+// device, 0 if the runtime reports none for one of them.
 int fused_pair_slots(int sms) {
   const int n = std::min(std::min(resident_pairs<FwdPairCfg>(), resident_pairs<BwdPairCfg>()),
                          std::min(resident_pairs<FwdPair2Cfg>(), resident_pairs<BwdPair2Cfg>()));
