@@ -69,9 +69,10 @@ class _DropoutDesc(ctypes.Structure):
 
 
 class Dropout(NamedTuple):
-    """Counter-based dropout: probability p in [0, 1), 64-bit seed and counter
-    offset (taken mod 2^64). The same three values give the same mask; a
-    tensor of n elements uses ceil(n / 8) counters from `offset` on."""
+    """Counter-based dropout: probability p in [0, 1 - 2^-17), taken to the
+    nearest 2^-16, 64-bit seed and counter offset (taken mod 2^64). The same
+    three values give the same mask; a tensor of n elements uses ceil(n / 8)
+    counters from `offset` on."""
     p: float
     seed: int
     offset: int = 0
@@ -513,9 +514,10 @@ def linear_bwd(packed, q, scale2, X, dY, A, B, alpha: float, N: int, K: int, XA=
 
 
 def dropout(x: torch.Tensor, drop: Dropout, out=None) -> torch.Tensor:
-    """D(x): kept elements times 1 / (1 - p), the others 0 (qlora_dropout), for
-    bf16, fp16 and fp32 tensors of any shape; out may be x. The backward of
-    y = D(x) is the same call on dy."""
+    """D(x): kept elements times 1 / (1 - p) (p to the nearest 2^-16), the others
+    0 (qlora_dropout), for contiguous, 16-byte aligned bf16, fp16 and fp32
+    tensors of any shape; out may be x and must not overlap it otherwise. The
+    backward of y = D(x) is the same call on dy."""
     if x.dtype not in _ELEMENT:
         raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
     _req(x, "x", x.dtype)

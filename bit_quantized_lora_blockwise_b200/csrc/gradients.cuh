@@ -4,10 +4,11 @@
 // the expert's tokens alone. skinny_kernel computes the same sums with one
 // cluster per tile, split over the tokens; with more tiles than resident CTAs
 // its cost is the CTA itself (tables, TMEM, first copies, shared-memory
-// reduction: some 10 us), not the sums. Here two CTAs per SM run over the
-// (product, expert, 128-row tile) units with the ring running on from one unit
-// to the next and two TMEM accumulators, so that a unit's readout overlaps the
-// next one's products. Bound by reading X and dY once.
+// reduction: some 10 us), not the sums. Here two CTAs per SM (one for more than
+// 64 ranks) run over the (product, expert, 128-row tile) units with the ring
+// running on from one unit to the next and two TMEM accumulators, so that a
+// unit's readout overlaps the next one's products. Bound by reading X and dY
+// once.
 //
 // The token rows are the MMA's K: MN-major operands, 64 tokens a stage, from
 // the expert's first row on (a row coordinate, aligned to nothing). The last
@@ -31,16 +32,18 @@
 // they need nothing from dX and fill the SMs that its last round leaves idle;
 // every role waits for dX before its first unit of dA. (8192 rows, 8 experts of
 // 4096 x 11008: with the generator evaluated here once more this launch ended
-// 100 us after dX, with the bits and the units handed out as below 52; without
-// dropout 22.)
+// 100 us after dX, with the bits and the units handed out as below 53; without
+// dropout 30.)
 //
 // Experts are uneven and a CTA has only a few units, so the units are handed
 // out as CTAs become free, the expert with the most tokens first, from a counter
-// in the workspace (with a fixed stride the SMs were active 69 % of the time). Warp 0 takes them and passes them on through a
-// small ring. Every unit's sums are its own, so who computes it changes nothing.
+// in the workspace (with a fixed stride the SMs were active 69 % of the time).
+// Warp 0 takes them and passes them on through a small ring. Every unit's sums
+// are its own, so who computes it changes nothing.
 //
-// Roles: warp 0 TMA, warp 1 TMEM + MMA, warp 2 tails, warp 3 zeros, warps 4-7 readout and
-// stores, warps 8-15 (DROP) take each landed stage of X through the mask.
+// Roles: warp 0 TMA, warp 1 TMEM + MMA, warp 2 tails, warp 3 zeros, warps 4-7
+// readout and stores, warps 8-15 (DROP) take each landed stage of X through the
+// mask.
 #pragma once
 
 #include "groups.cuh"

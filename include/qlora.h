@@ -257,7 +257,7 @@ QLORA_API qlora_status qlora_linear_bwd_dt(const uint8_t *packed, const uint8_t 
  * The device error word of the current device: bit 0 = a bounded pipeline
  * wait ran out (the kernel returned early; its outputs are undefined);
  * bit 1 = expert offsets were not ascending within [0, T]
- * (qlora_grouped_linear_fwd). Synchronizes the device. clear != 0 resets the
+ * (qlora_grouped_linear_fwd and _bwd). Synchronizes the device. clear != 0 resets the
  * word. Returns 0xFFFFFFFF if the word cannot be read.
  */
 QLORA_API uint32_t qlora_device_error(int clear);
@@ -503,15 +503,16 @@ QLORA_API qlora_status qlora_dropout(const void *x, void *y, int64_t n, qlora_el
  * Accumulation is fp32. s XA (XA = D(X) A) and, for dX, G are rounded to 16
  * bits before their rank-r products; dA takes G in two 16-bit parts, which lose
  * nothing that its own rounding keeps, down to |G| of 2^-25 in fp16. Everything
- * else is rounded once; the dropout factor is applied in fp32. Experts are isolated: a NaN or an
- * infinity in one expert's rows or adapters reaches that expert's outputs
- * only.
+ * else is rounded once; the dropout factor multiplies fp32 sums. Experts are
+ * isolated: a NaN or an infinity in one expert's rows or adapters reaches that
+ * expert's outputs only.
  * Requires 1 <= E <= QLORA_MAX_EXPERTS, T >= 0 (T = 0: token pointers may be
  * NULL; the backward zeroes dA and dB), N, K >= 64 and multiples of 64,
- * E N and E K at most 2^30, 1 <= r <= 256, r % 8 == 0, alpha finite, 16-byte
- * aligned pointers (offsets: 4). Outputs must not overlap inputs or each
- * other. Both calls can be captured into a CUDA graph after one uncaptured
- * call of the same kind.
+ * T, E N and E K at most 2^30, (min(E, T) + T / 256) ceil(max(N, K) / 128) at
+ * most 2^27 (token tiles times weight tiles), 1 <= r <= 256, r % 8 == 0, alpha
+ * finite, 16-byte aligned pointers (offsets: 4). Outputs must not overlap inputs
+ * or each other. Both calls can be captured into a CUDA graph after one
+ * uncaptured call of the same kind.
  */
 #define QLORA_MAX_EXPERTS 1024
 QLORA_API size_t qlora_grouped_workspace_bytes(int E, int64_t T, int64_t N, int64_t K, int r, int dropout);
